@@ -316,6 +316,74 @@ more_status more_route_backward(const void* X, const void* R1, const void* R2, i
                                 float* out_R2bar, float* out_g, void* scratch, size_t scratch_bytes,
                                 void* stream);
 
+/*
+ * The experts behind the router (MoRE §2 "MoE layer"; App. E, Fig. 9): gated linear units, two products an
+ * expert.  With W_up[e] = [A_e; B_e], e = idx[n][j] and g = gate[n][j],
+ *   out[n] = sum_j g W_down[e] (silu(A_e x_n) * (B_e x_n)),     silu(a) = a / (1 + exp(-a)).
+ *   X        bf16 [N][h]
+ *   W_up     bf16 [M][2 s][h]   rows 0 .. s - 1 of an expert: A_e; rows s .. 2 s - 1: B_e
+ *   W_down   bf16 [M][h][s]
+ *   gate     fp32 [N][k]        as more_route writes it
+ *   offsets  int32 [M + 1], slots int32 [N k]   as more_dispatch writes them; a slot is listed at most once
+ *   out      bf16 [N][h]        overwritten; a token none of whose slots is listed gets zeros
+ * Both products are accumulated in fp32; silu(A x) * (B x) and each slot's row of the second product, already
+ * times its gate, are rounded to bf16, and a token's k rows are summed in fp32 in the order of j.  The result does
+ * not depend on the launch.
+ * Offsets that fall or lie outside [0, N k] give zeros, and a slot outside [0, N k) is skipped; both set
+ * MORE_DEVERR_BAD_INPUT.
+ * scratch: device, 16-byte aligned, at least more_experts_scratch_bytes(N, h, s, M, k) bytes (0: not supported); calls
+ * that may overlap need one each.  Its contents need no initialisation.
+ * Requirements: N >= 0; h and s multiples of 8; 1 <= k <= M, k <= MORE_KMAX; M <= MORE_MMAX; h, s <= 131072; W_up, W_down
+ * and offsets non-NULL, the other pointers non-NULL unless N == 0; every pointer 16-byte aligned.  Rows and tiles count
+ * in 32 bits: N k + 15 min(M, N k) < 2^31 among others (else MORE_ERR_UNSUPPORTED).  Asynchronous on `stream`; allocates
+ * nothing; may be captured into a graph.
+ */
+size_t more_experts_scratch_bytes(int64_t N, int h, int s, int M, int k);
+more_status more_experts(const void* X, const void* W_up, const void* W_down, int64_t N, int h, int s, int M, int k,
+                         const float* gate, const int32_t* offsets, const int32_t* slots, void* out, void* scratch,
+                         size_t scratch_bytes, void* stream);
+
+/*
+ * Rows in 8 bits, symmetric: with t the largest magnitude of a row, out_q = round(127 v / t) (halves to even) and
+ * out_scale = t / 127; a row of zeros has scale 0.  V: bf16 [rows][width], finite, magnitudes up to 2^120; width a
+ * multiple of 16.  For the weights of more_experts_int8 take their rows as they lie: M 2 s rows of width h, and M h
+ * rows of width s.
+ */
+more_status more_quantize_rows(const void* V, int64_t rows, int width, int8_t* out_q, float* out_scale, void* stream);
+
+/*
+ * more_experts with 8-bit operands: W_up int8 [M][2 s][h] and W_down int8 [M][h][s] with a scale per output channel
+ * (up_scale fp32 [M][2 s], down_scale fp32 [M][h]; as more_quantize_rows gives them), and x and silu(A x) * (B x)
+ * rounded to 8 bits by the same rule, a scale per row, before each product.  Products are summed exactly in 32-bit
+ * integers, everything between them is fp32.  h and s are multiples of 16; else as more_experts.
+ */
+size_t more_experts_int8_scratch_bytes(int64_t N, int h, int s, int M, int k);
+more_status more_experts_int8(const void* X, const int8_t* W_up, const float* up_scale, const int8_t* W_down,
+                              const float* down_scale, int64_t N, int h, int s, int M, int k, const float* gate,
+                              const int32_t* offsets, const int32_t* slots, void* out, void* scratch,
+                              size_t scratch_bytes, void* stream);
+
+/*
+ * Backward of more_experts: with y the output and L a loss, out_bar = dL/dy (bf16 [N][h]), the activations
+ * recomputed from X.  Writes (never adds to)
+ *   out_Xbar        bf16 [N][h]        the experts' share of dL/dX (the router's is more_route_backward's)
+ *   out_W_up_bar    bf16 [M][2 s][h]   zeros for an expert without a slot
+ *   out_W_down_bar  bf16 [M][h][s]     the same
+ *   out_gate_bar    fp32 [N][k]        dL/dgate
+ *   out_logits_bar  fp32 [N][k]        dL/d(selected logits) = gate_j (gate_bar_j - sum_i gate_i gate_bar_i): the
+ *                                      top_vals_bar of more_route_backward
+ * Products are accumulated in fp32; the gradients of A x, B x and gate * silu(A x) * (B x), and each slot's row of the
+ * X gradient, are rounded to bf16; the gates' gradients are fp32 throughout.  No atomics: the result does not depend
+ * on the launch.  Other arguments and requirements as for more_experts, with
+ * more_experts_backward_scratch_bytes; N == 0 zeroes the weights' gradients.
+ */
+size_t more_experts_backward_scratch_bytes(int64_t N, int h, int s, int M, int k);
+more_status more_experts_backward(const void* X, const void* W_up, const void* W_down, int64_t N, int h, int s, int M,
+                                  int k, const float* gate, const int32_t* offsets, const int32_t* slots,
+                                  const void* out_bar, void* out_Xbar, void* out_W_up_bar, void* out_W_down_bar,
+                                  float* out_gate_bar, float* out_logits_bar, void* scratch, size_t scratch_bytes,
+                                  void* stream);
+
 /* MORE_ROUTE_ABI_VERSION of the built library. */
 int more_abi_version(void);
 

@@ -22,6 +22,8 @@ from . import _build
 
 __all__ = ["route", "auto_variant", "route_fullrank", "selftest_wait_timeout", "route_train", "route_backward", "route_backward_scratch_bytes", "dispatch",
            "dispatch_scratch_bytes", "route_unfused", "route_unfused_tc", "route_unfused_static", "unfused_scratch_bytes", "device_status",
+           "experts", "experts_scratch_bytes", "experts_backward", "experts_backward_scratch_bytes", "experts_int8",
+           "experts_int8_scratch_bytes", "quantize_rows",
            "Router", "MoreError", "VARIANTS", "library_path", "abi_version", "KMAX", "STATS_MMAX"]
 
 KMAX = 16
@@ -73,6 +75,16 @@ def _load_library() -> ctypes.CDLL:
     lib.more_route_backward.argtypes = [P, P, P, I64, I, I, I, I] + [P] * 10 + [ctypes.c_size_t, P]
     lib.more_route_unfused_scratch_bytes.restype = ctypes.c_size_t
     lib.more_route_unfused_scratch_bytes.argtypes = [I64, I, I]
+    for name in ("more_experts", "more_experts_int8", "more_experts_backward"):
+        getattr(lib, name + "_scratch_bytes").restype = ctypes.c_size_t
+        getattr(lib, name + "_scratch_bytes").argtypes = [I64, I, I, I, I]
+        getattr(lib, name).restype = I
+    tail = [P, ctypes.c_size_t, P]
+    lib.more_experts.argtypes = [P, P, P, I64, I, I, I, I, P, P, P, P] + tail
+    lib.more_experts_int8.argtypes = [P, P, P, P, P, I64, I, I, I, I, P, P, P, P] + tail
+    lib.more_experts_backward.argtypes = [P, P, P, I64, I, I, I, I] + [P] * 9 + tail
+    lib.more_quantize_rows.restype = I
+    lib.more_quantize_rows.argtypes = [P, I64, I, P, P, P]
     lib.more_device_status.restype = I
     lib.more_device_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
     lib.more_status_string.restype = ctypes.c_char_p
@@ -259,6 +271,151 @@ def dispatch(idx: torch.Tensor, M: int, *, scratch: torch.Tensor | None = None, 
                                     scratch.numel(), DISPATCH_VARIANTS[variant], _stream_handle(stream))
     _check(st, "more_dispatch")
     return out_offsets, out_sorted
+
+
+def _on_device(first: torch.Tensor, stream, **tensors):
+    """Checks that every tensor lies on the device of ``first``, and gives that device's context and stream."""
+    for name, t in tensors.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, X on {first.device}")
+    if stream is not None and stream.device != first.device:
+        raise ValueError(f"the stream is on {stream.device}, X on {first.device}")
+    return torch.cuda.device(first.device), torch.cuda.current_stream(first.device) if stream is None else stream
+
+
+def _typed(t, name, dtype, shape):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _output(t, name, dtype, shape, device):
+    return torch.empty(shape, dtype=dtype, device=device) if t is None else _typed(t, name, dtype, shape)
+
+
+def _scratch(t, need, device):
+    if t is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    if not t.is_cuda or not t.is_contiguous() or t.dtype != torch.uint8:
+        raise ValueError("scratch must be a contiguous uint8 CUDA tensor")
+    return t
+
+
+def _expert_shapes(X, W_up, W_down, gate, offsets, slots, dtype):
+    if X.dim() != 2 or W_up.dim() != 3 or W_down.dim() != 3 or gate.dim() != 2:
+        raise ValueError("X and gate are matrices, W_up and W_down one matrix per expert")
+    _as_bf16(X, "X")
+    N, h = X.shape
+    M, s = W_down.shape[0], W_down.shape[2]
+    k = gate.shape[1]
+    _typed(W_up, "W_up", dtype, (M, 2 * s, h))
+    _typed(W_down, "W_down", dtype, (M, h, s))
+    _typed(gate, "gate", torch.float32, (N, k))
+    _typed(offsets, "offsets", torch.int32, (M + 1,))
+    _typed(slots, "slots", torch.int32, (N * k,))
+    return N, h, s, M, k
+
+
+def experts_scratch_bytes(N: int, h: int, s: int, M: int, k: int) -> int:
+    return int(_lib.more_experts_scratch_bytes(N, h, s, M, k))
+
+
+def experts(X: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tensor, gate: torch.Tensor, offsets: torch.Tensor,
+            slots: torch.Tensor, *, out=None, scratch: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The experts behind the router (§2 "MoE layer"; App. E, Fig. 9): for token n the sum over its selections j of
+    ``gate[n, j] * W_down[e] @ (silu(A_e x) * (B_e x))`` with ``W_up[e] = [A_e; B_e]``.
+
+    X bf16 [N, h]; W_up bf16 [M, 2 s, h]; W_down bf16 [M, h, s]; gate fp32 [N, k] from :func:`route`;
+    ``offsets, slots`` from :func:`dispatch`.  Returns bf16 [N, h].  h and s are multiples of 8.
+    """
+    N, h, s, M, k = _expert_shapes(X, W_up, W_down, gate, offsets, slots, torch.bfloat16)
+    device, stream = _on_device(X, stream, W_up=W_up, W_down=W_down, gate=gate, offsets=offsets, slots=slots, out=out,
+                                scratch=scratch)
+    with device, torch.cuda.stream(stream):
+        out = _output(out, "out", torch.bfloat16, (N, h), X.device)
+        scratch = _scratch(scratch, experts_scratch_bytes(N, h, s, M, k), X.device)
+        st = _lib.more_experts(_ptr(X), _ptr(W_up), _ptr(W_down), N, h, s, M, k, _ptr(gate), _ptr(offsets),
+                               _ptr(slots), _ptr(out), _ptr(scratch), scratch.numel(), _stream_handle(stream))
+    _check(st, "more_experts")
+    return out
+
+
+def quantize_rows(V: torch.Tensor, *, out_q=None, out_scale=None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Rows of V (bf16 [..., width], width a multiple of 16) in 8 bits: ``(q int8 [..., width], scale fp32 [...])``
+    with ``q = round(127 v / max|v|)``, halves to even, and ``scale = max|v| / 127``.  The weights of
+    :func:`experts_int8` are ``quantize_rows(W_up)`` and ``quantize_rows(W_down)``."""
+    V = _as_bf16(V, "V")
+    if V.dim() < 1:
+        raise ValueError("V must have rows")
+    device, stream = _on_device(V, stream, out_q=out_q, out_scale=out_scale)
+    with device, torch.cuda.stream(stream):
+        out_q = _output(out_q, "out_q", torch.int8, V.shape, V.device)
+        out_scale = _output(out_scale, "out_scale", torch.float32, V.shape[:-1], V.device)
+        width = V.shape[-1]
+        st = _lib.more_quantize_rows(_ptr(V), V.numel() // max(width, 1), width, _ptr(out_q), _ptr(out_scale),
+                                     _stream_handle(stream))
+    _check(st, "more_quantize_rows")
+    return out_q, out_scale
+
+
+def experts_int8_scratch_bytes(N: int, h: int, s: int, M: int, k: int) -> int:
+    return int(_lib.more_experts_int8_scratch_bytes(N, h, s, M, k))
+
+
+def experts_int8(X: torch.Tensor, W_up: torch.Tensor, up_scale: torch.Tensor, W_down: torch.Tensor,
+                 down_scale: torch.Tensor, gate: torch.Tensor, offsets: torch.Tensor, slots: torch.Tensor, *, out=None,
+                 scratch: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """:func:`experts` with 8-bit operands: W_up int8 [M, 2 s, h] and W_down int8 [M, h, s] with a scale per output
+    channel (``up_scale`` fp32 [M, 2 s], ``down_scale`` fp32 [M, h]; :func:`quantize_rows`), x and the middle rounded to
+    8 bits with a scale per row before each product.  h and s are multiples of 16."""
+    N, h, s, M, k = _expert_shapes(X, W_up, W_down, gate, offsets, slots, torch.int8)
+    _typed(up_scale, "up_scale", torch.float32, (M, 2 * s))
+    _typed(down_scale, "down_scale", torch.float32, (M, h))
+    device, stream = _on_device(X, stream, W_up=W_up, up_scale=up_scale, W_down=W_down, down_scale=down_scale, gate=gate,
+                                offsets=offsets, slots=slots, out=out, scratch=scratch)
+    with device, torch.cuda.stream(stream):
+        out = _output(out, "out", torch.bfloat16, (N, h), X.device)
+        scratch = _scratch(scratch, experts_int8_scratch_bytes(N, h, s, M, k), X.device)
+        st = _lib.more_experts_int8(_ptr(X), _ptr(W_up), _ptr(up_scale), _ptr(W_down), _ptr(down_scale), N, h, s, M, k,
+                                    _ptr(gate), _ptr(offsets), _ptr(slots), _ptr(out), _ptr(scratch), scratch.numel(),
+                                    _stream_handle(stream))
+    _check(st, "more_experts_int8")
+    return out
+
+
+def experts_backward_scratch_bytes(N: int, h: int, s: int, M: int, k: int) -> int:
+    return int(_lib.more_experts_backward_scratch_bytes(N, h, s, M, k))
+
+
+def experts_backward(X: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tensor, gate: torch.Tensor,
+                     offsets: torch.Tensor, slots: torch.Tensor, out_bar: torch.Tensor, *, out_Xbar=None,
+                     out_W_up_bar=None, out_W_down_bar=None, out_gate_bar=None, out_logits_bar=None,
+                     scratch: torch.Tensor | None = None, stream=None):
+    """Backward of :func:`experts` from ``out_bar`` (bf16 [N, h], the gradient on its output), the activations
+    recomputed from X.  Returns ``(Xbar bf16 [N, h], W_up_bar bf16 [M, 2 s, h], W_down_bar bf16 [M, h, s], gate_bar
+    fp32 [N, k], logits_bar fp32 [N, k])``; the last is the gradient on the selected logits, the ``top_vals_bar`` of
+    :func:`route_backward`, which adds the router's share of the X gradient."""
+    N, h, s, M, k = _expert_shapes(X, W_up, W_down, gate, offsets, slots, torch.bfloat16)
+    _typed(out_bar, "out_bar", torch.bfloat16, (N, h))
+    device, stream = _on_device(X, stream, W_up=W_up, W_down=W_down, gate=gate, offsets=offsets, slots=slots,
+                                out_bar=out_bar, out_Xbar=out_Xbar, out_W_up_bar=out_W_up_bar,
+                                out_W_down_bar=out_W_down_bar, out_gate_bar=out_gate_bar, out_logits_bar=out_logits_bar,
+                                scratch=scratch)
+    with device, torch.cuda.stream(stream):
+        bf16, f32 = torch.bfloat16, torch.float32
+        outs = (_output(out_Xbar, "out_Xbar", bf16, (N, h), X.device),
+                _output(out_W_up_bar, "out_W_up_bar", bf16, W_up.shape, X.device),
+                _output(out_W_down_bar, "out_W_down_bar", bf16, W_down.shape, X.device),
+                _output(out_gate_bar, "out_gate_bar", f32, (N, k), X.device),
+                _output(out_logits_bar, "out_logits_bar", f32, (N, k), X.device))
+        scratch = _scratch(scratch, experts_backward_scratch_bytes(N, h, s, M, k), X.device)
+        st = _lib.more_experts_backward(_ptr(X), _ptr(W_up), _ptr(W_down), N, h, s, M, k, _ptr(gate), _ptr(offsets),
+                                        _ptr(slots), _ptr(out_bar), *(_ptr(t) for t in outs), _ptr(scratch),
+                                        scratch.numel(), _stream_handle(stream))
+    _check(st, "more_experts_backward")
+    return outs
 
 
 def auto_variant(N: int, h: int, r: int, M: int, k: int) -> str | None:

@@ -1,6 +1,7 @@
 // C ABI of the router: argument validation, variant choice, the device error word.
 #include <mutex>
 
+#include "experts_internal.cuh"
 #include "more_internal.cuh"
 
 namespace more {
@@ -347,6 +348,156 @@ more_status more_route_fullrank(const void* X, const void* W, int64_t N, int h, 
     return MORE_ERR_CUDA;
   if (N == 0) return MORE_OK;
   return launch_fullrank(a) == cudaSuccess ? MORE_OK : MORE_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace more {
+namespace {
+
+// Argument checks shared by the experts' entry points; `unit`: what h and s are multiples of (16-byte rows).
+more_status validate_experts(const ExpertsArgs& a, int unit, size_t scratch_bytes, int kind) {
+  if (a.N < 0 || a.h < unit || a.h % unit || a.s < unit || a.s % unit || a.M < 1 || a.k < 1 || a.k > a.M)
+    return MORE_ERR_INVALID_ARG;
+  const bool int8 = kind == 1, backward = kind == 2;
+  if (!a.W_up || !a.W_down || !a.offsets || (int8 && (!a.up_scale || !a.down_scale)) ||
+      (backward && (!a.W_up_bar || !a.W_down_bar)))
+    return MORE_ERR_INVALID_ARG;
+  if (a.N > 0 && (!a.X || !a.gate || !a.slots || !a.out || !a.scratch ||
+                  (backward && (!a.out_bar || !a.gate_bar || !a.logits_bar))))
+    return MORE_ERR_INVALID_ARG;
+  const void* ptrs[] = {a.X,   a.W_up,    a.W_down,   a.up_scale,   a.down_scale, a.gate,       a.offsets, a.slots,
+                        a.out, a.out_bar, a.W_up_bar, a.W_down_bar, a.gate_bar,   a.logits_bar, a.scratch};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return MORE_ERR_INVALID_ARG;
+  if (!experts_supported(a.N, a.h, a.s, a.M, a.k)) return MORE_ERR_UNSUPPORTED;
+  if (a.N > 0 && scratch_bytes < experts_scratch(a.N, a.h, a.s, a.M, a.k, kind)) return MORE_ERR_INVALID_ARG;
+  return MORE_OK;
+}
+
+size_t experts_scratch_checked(int64_t N, int h, int s, int M, int k, int kind) {
+  if (N < 0 || h < 1 || s < 1 || M < 1 || k < 1 || !experts_supported(N, h, s, M, k)) return 0;
+  return experts_scratch(N, h, s, M, k, kind);
+}
+
+}  // namespace
+}  // namespace more
+
+extern "C" {
+
+size_t more_experts_scratch_bytes(int64_t N, int h, int s, int M, int k) {
+  return experts_scratch_checked(N, h, s, M, k, 0);
+}
+
+more_status more_experts(const void* X, const void* W_up, const void* W_down, int64_t N, int h, int s, int M, int k,
+                         const float* gate, const int32_t* offsets, const int32_t* slots, void* out, void* scratch,
+                         size_t scratch_bytes, void* stream) {
+  ExpertsArgs a = {};
+  a.X = X;
+  a.W_up = W_up;
+  a.W_down = W_down;
+  a.N = N;
+  a.h = h;
+  a.s = s;
+  a.M = M;
+  a.k = k;
+  a.gate = gate;
+  a.offsets = offsets;
+  a.slots = slots;
+  a.out = out;
+  a.scratch = scratch;
+  a.stream = static_cast<cudaStream_t>(stream);
+  const more_status st = validate_experts(a, 8, scratch_bytes, 0);
+  if (st != MORE_OK || N == 0) return st;
+  a.status = status_word();
+  if (!a.status) return MORE_ERR_CUDA;
+  return launch_experts(a) == cudaSuccess ? MORE_OK : MORE_ERR_CUDA;
+}
+
+size_t more_experts_int8_scratch_bytes(int64_t N, int h, int s, int M, int k) {
+  return experts_scratch_checked(N, h, s, M, k, 1);
+}
+
+more_status more_experts_int8(const void* X, const int8_t* W_up, const float* up_scale, const int8_t* W_down,
+                              const float* down_scale, int64_t N, int h, int s, int M, int k, const float* gate,
+                              const int32_t* offsets, const int32_t* slots, void* out, void* scratch,
+                              size_t scratch_bytes, void* stream) {
+  ExpertsArgs a = {};
+  a.X = X;
+  a.W_up = W_up;
+  a.W_down = W_down;
+  a.up_scale = up_scale;
+  a.down_scale = down_scale;
+  a.N = N;
+  a.h = h;
+  a.s = s;
+  a.M = M;
+  a.k = k;
+  a.gate = gate;
+  a.offsets = offsets;
+  a.slots = slots;
+  a.out = out;
+  a.scratch = scratch;
+  a.stream = static_cast<cudaStream_t>(stream);
+  const more_status st = validate_experts(a, 16, scratch_bytes, 1);
+  if (st != MORE_OK || N == 0) return st;
+  a.status = status_word();
+  if (!a.status) return MORE_ERR_CUDA;
+  return launch_experts_int8(a) == cudaSuccess ? MORE_OK : MORE_ERR_CUDA;
+}
+
+more_status more_quantize_rows(const void* V, int64_t rows, int width, int8_t* out_q, float* out_scale, void* stream) {
+  if (rows < 0 || width < 16 || width % 16 || (rows > 0 && (!V || !out_q || !out_scale))) return MORE_ERR_INVALID_ARG;
+  if ((V && !aligned16(V)) || (out_q && !aligned16(out_q)) || (out_scale && !aligned16(out_scale)))
+    return MORE_ERR_INVALID_ARG;
+  if (rows > 0x7fffffffLL) return MORE_ERR_UNSUPPORTED;
+  return launch_quantize_bf16(static_cast<const __nv_bfloat16*>(V), rows, width, out_q, out_scale,
+                              static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MORE_OK
+             : MORE_ERR_CUDA;
+}
+
+size_t more_experts_backward_scratch_bytes(int64_t N, int h, int s, int M, int k) {
+  return experts_scratch_checked(N, h, s, M, k, 2);
+}
+
+more_status more_experts_backward(const void* X, const void* W_up, const void* W_down, int64_t N, int h, int s, int M,
+                                  int k, const float* gate, const int32_t* offsets, const int32_t* slots,
+                                  const void* out_bar, void* out_Xbar, void* out_W_up_bar, void* out_W_down_bar,
+                                  float* out_gate_bar, float* out_logits_bar, void* scratch, size_t scratch_bytes,
+                                  void* stream) {
+  ExpertsArgs a = {};
+  a.X = X;
+  a.W_up = W_up;
+  a.W_down = W_down;
+  a.N = N;
+  a.h = h;
+  a.s = s;
+  a.M = M;
+  a.k = k;
+  a.gate = gate;
+  a.offsets = offsets;
+  a.slots = slots;
+  a.out = out_Xbar;
+  a.out_bar = out_bar;
+  a.W_up_bar = out_W_up_bar;
+  a.W_down_bar = out_W_down_bar;
+  a.gate_bar = out_gate_bar;
+  a.logits_bar = out_logits_bar;
+  a.scratch = scratch;
+  a.stream = static_cast<cudaStream_t>(stream);
+  const more_status st = validate_experts(a, 8, scratch_bytes, 2);
+  if (st != MORE_OK) return st;
+  if (N == 0) {
+    const size_t each = (size_t)M * h * s * 2;
+    return cudaMemsetAsync(out_W_up_bar, 0, 2 * each, a.stream) == cudaSuccess &&
+                   cudaMemsetAsync(out_W_down_bar, 0, each, a.stream) == cudaSuccess
+               ? MORE_OK
+               : MORE_ERR_CUDA;
+  }
+  a.status = status_word();
+  if (!a.status) return MORE_ERR_CUDA;
+  return launch_experts_backward(a) == cudaSuccess ? MORE_OK : MORE_ERR_CUDA;
 }
 
 more_status more_selftest_wait_timeout(int32_t* out_result, void* stream) {

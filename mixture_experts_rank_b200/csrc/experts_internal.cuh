@@ -1,0 +1,113 @@
+// Shared declarations of the experts' operators: the padded row layout that every product works on,
+// its place in the caller's scratch, and the launchers.
+//
+// The slots sorted by expert (more_dispatch) are laid out as rows, each expert's rows starting at a
+// multiple of 16 (kRowPad: the K step of a 16-bit MMA, so that a product over an expert's rows can
+// end on a whole step, and a quad of rows is one gathered TMA load).  A tile is up to 128 rows of one
+// expert.  Padding rows repeat the expert's last token and carry slot -1.
+#pragma once
+#include "more_internal.cuh"
+
+namespace more {
+
+constexpr int kRowPad = 16;
+constexpr int kTileRows = 128;
+
+// Where a call's rows come from; all pointers are in the caller's scratch.
+struct Rows {
+  int32_t* row_slot;   // [R] slot of a row, -1 for padding (and for a slot outside [0, S))
+  int32_t* row_token;  // [R] token of a row (any valid token where row_slot < 0)
+  float* row_gate;     // [R] gate of a row's slot (0 where row_slot < 0)
+  int32_t* slot_row;   // [S] row of a slot, -1 where no expert lists it
+  int4* tiles;         // [T] {expert, first row, rows that are slots, rows rounded up to kRowPad}
+  int32_t* row_start;  // [M + 1] first row of each expert
+  int32_t* n_tiles;    // [1]
+};
+
+// One call of the experts' operators after validation.
+struct ExpertsArgs {
+  const void* X;         // bf16 [N][h]
+  const void* W_up;      // bf16 or int8 [M][2 s][h]
+  const void* W_down;    // bf16 or int8 [M][h][s]
+  const float* up_scale;    // [M][2 s], int8 weights only
+  const float* down_scale;  // [M][h], int8 weights only
+  const float* gate;        // [N][k]
+  const int32_t* offsets;   // [M + 1]
+  const int32_t* slots;     // [N k]
+  int64_t N;
+  int h, s, M, k;
+  void* out;  // bf16 [N][h]
+  // backward
+  const void* out_bar;  // bf16 [N][h]
+  void* W_up_bar;       // bf16 [M][2 s][h]
+  void* W_down_bar;     // bf16 [M][h][s]
+  float* gate_bar;      // [N][k]
+  float* logits_bar;    // [N][k]
+  void* scratch;
+  unsigned int* status;
+  cudaStream_t stream;
+  int64_t S() const { return N * k; }
+};
+
+// Upper bounds over every routing of S slots to M experts.
+inline int64_t max_rows(int64_t S, int M) {
+  const int64_t used = S < M ? S : M;
+  return (S + used * (kRowPad - 1) + kTileRows - 1) / kTileRows * kTileRows;
+}
+inline int64_t max_tiles(int64_t S, int M) { return S / kTileRows + (S < M ? S : M); }
+
+// Rows, tiles and work items of every kernel count in 32 bits.
+inline bool experts_supported(int64_t N, int h, int s, int M, int k) {
+  constexpr int64_t most = 0x7fffffffLL;
+  if (k > MORE_KMAX || M > MORE_MMAX || N > most / k || h > 131072 || s > 131072) return false;
+  const int64_t S = N * k, wide = (h > 2 * s ? h : 2 * s) / 64 + 1;
+  return max_rows(S, M) + kTileRows < most && (max_tiles(S, M) + 1) * wide < most &&
+         (int64_t)M * (2 * (int64_t)s / 128 + 1) * (h / 128 + 1) < most;
+}
+
+// Hands out aligned pieces of a scratch buffer; with a null base it only counts bytes.
+struct Carver {
+  uint8_t* base;
+  size_t used = 0;
+  explicit Carver(void* b) : base(static_cast<uint8_t*>(b)) {}
+  template <class T>
+  T* take(int64_t n) {
+    T* p = reinterpret_cast<T*>(base + used);
+    used += ((size_t)n * sizeof(T) + 255) / 256 * 256;
+    return base ? p : nullptr;
+  }
+};
+
+inline Rows carve_rows(Carver& c, int64_t S, int M) {
+  Rows r;
+  const int64_t R = max_rows(S, M);
+  r.row_slot = c.take<int32_t>(R);
+  r.row_token = c.take<int32_t>(R);
+  r.row_gate = c.take<float>(R);
+  r.slot_row = c.take<int32_t>(S);
+  r.tiles = c.take<int4>(max_tiles(S, M));
+  r.row_start = c.take<int32_t>((int64_t)M + 1);
+  r.n_tiles = c.take<int32_t>(1);
+  return r;
+}
+
+// Lays the rows out from offsets, slots and gates (experts_rows.cu).
+cudaError_t launch_rows(const ExpertsArgs& a, const Rows& r);
+// out[n] = sum over j of y[slot_row[n k + j]], fp32 sums in the order of j, rounded once to bf16.
+cudaError_t launch_combine(const ExpertsArgs& a, const Rows& r, const __nv_bfloat16* y, void* out);
+// gate_bar[slot] = the sum of `parts` partial sums [parts][R] in order, and the logits' gradient
+// of a softmax over the k gates.
+cudaError_t launch_gate_grads(const ExpertsArgs& a, const Rows& r, const float* part, int parts, int64_t R);
+// Symmetric 8-bit rounding of rows: scale = max |v| / 127, q = round-half-even(127 v / max |v|).
+cudaError_t launch_quantize_bf16(const __nv_bfloat16* v, int64_t rows, int width, int8_t* q, float* scale,
+                                 cudaStream_t stream);
+// The same for the rows that a call uses of an fp32 [R][width] buffer (every tile's slots).
+cudaError_t launch_quantize_rows(const ExpertsArgs& a, const Rows& r, const float* v, int width, int8_t* q,
+                                 float* scale);
+
+size_t experts_scratch(int64_t N, int h, int s, int M, int k, int kind);  // kind: 0 bf16, 1 int8, 2 backward
+cudaError_t launch_experts(const ExpertsArgs& a);
+cudaError_t launch_experts_int8(const ExpertsArgs& a);
+cudaError_t launch_experts_backward(const ExpertsArgs& a);
+
+}  // namespace more

@@ -1,0 +1,799 @@
+// The experts' matrix products on the tensor cores, grouped by expert.
+//
+// With x_t the row of token t, (A; B) = W_up[e] and D = W_down[e]:
+//   up        H = silu(x A^T) * (x B^T)                     rows gathered from X by token
+//   down      Y = gate * H D^T                              rows of H
+//   backward  with a = x A^T, b = x B^T, G = y_bar D (rows of y_bar gathered by token), m = silu(a) * b:
+//             the gate's gradient sum(G * m), gate * m, and the gradients of a and b,
+//             gate * G * b * silu'(a) and gate * G * silu(a)
+//   dx        [da, db] W_up[e]                              rows of [da, db]
+//   dw up     [da, db]^T x                                  contracted over the expert's rows
+//   dw down   y_bar^T (gate * m)
+// and up8 / down8, the first two with 8-bit operands and the scales of rows and columns in the epilogue.
+//
+// A CTA holds 128 rows of one expert (128 output channels for the weights' gradients) on the TMEM lanes and up
+// to 256 columns:
+//   warp 0       TMA: stages of 128 bytes of K (64 values of 16 bits, 128 of 8), 128B-swizzled; rows that are
+//                picked by token come by gathered loads, one quad of rows a lane;
+//   warp 1       tcgen05 MMAs into two accumulators in TMEM, so a tile's epilogue runs under the next one's products;
+//   warps 4-11   epilogue, two warps a lane group.
+// The grid is persistent; tiles come from the row layout that the same call made on the device.
+// H and [da, db] are rounded to bf16: they are MMA operands.  Y and the rows of dx are rounded to bf16 before the
+// sum over a token's slots, which halves the traffic that bounds these kernels; the sum itself is in fp32.
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
+#include "experts_internal.cuh"
+#include "mbar_wait.cuh"
+#include "sm100_ptx.cuh"
+
+namespace more {
+namespace experts {
+
+using namespace sm100;
+
+enum Mode { kUp, kDown, kUp8, kDown8, kBack, kDx, kDwUp, kDwDown };
+
+constexpr int kThreads = 12 * 32;
+constexpr int kEpiWarps = 8;
+constexpr uint32_t kABytes = kTileRows * 128;  // 16 KB: 128 rows (or 2 boxes of 64 channels x 64 rows) of a stage
+constexpr uint32_t kBox = 64 * 128;            // 8 KB: a box of 64 rows x 128 bytes
+constexpr uint32_t kStageOut = 32 * 128;       // a warp's staging: 32 rows x 64 bf16 columns
+constexpr int kMaxStages = 6;
+
+template <int MODE, int HALF>
+struct Shape {
+  static constexpr bool kEight = MODE == kUp8 || MODE == kDown8;
+  static constexpr bool kIsUp = MODE == kUp || MODE == kUp8;
+  static constexpr bool kIsDown = MODE == kDown || MODE == kDown8;
+  static constexpr bool kIsDw = MODE == kDwUp || MODE == kDwDown;
+  static constexpr bool kStaged = kIsDown || MODE == kDx || kIsDw;  // epilogue goes through shared memory
+  // columns of one accumulator, and its place in TMEM
+  static constexpr int kCols = kIsUp ? 2 * HALF : MODE == kBack ? 3 * HALF : 256;
+  static constexpr int kAccStride = kCols <= 128 ? 128 : 256;
+  static constexpr uint32_t kTmemCols = 2 * kAccStride;
+  static constexpr int kBN = kIsUp || MODE == kBack ? HALF : 256;  // output columns of a tile
+  static constexpr uint32_t kBBytes = kIsUp || MODE == kBack ? 2 * HALF * 128 : 256 * 128;
+  static constexpr uint32_t kStage = kABytes + kBBytes;
+  static constexpr int kStages = kStage > 32 * 1024 ? 4 : 6;
+  static constexpr int kKBlock = kEight ? 128 : 64;
+  static constexpr int kKStep = kEight ? 32 : 16;
+  static constexpr uint32_t kOffOut = kStages * kStage;
+  static constexpr uint32_t kOffBar = kOffOut + (kStaged ? kEpiWarps * kStageOut : 0);
+  static constexpr uint32_t kSmem = kOffBar + (2 * kMaxStages + 4 + 1) * 8 + 16 + 1024;
+};
+
+struct Params {
+  Rows rows;
+  int64_t R;      // rows of the row buffers (a column of `part`)
+  int nc;         // tiles along the columns
+  int nm;         // tiles along the channels (weights' gradients)
+  int items;      // weights' gradients: M * nm * nc
+  int k1, k2;     // contracted lengths (k2: the second product of kBack)
+  int s, h;
+  int cols;       // output columns
+  void* out;      // kUp: H; kUp8: H in fp32; kDown, kDx: rows of h; kBack: [da, db]
+  __nv_bfloat16* out2;  // kBack: gate * m
+  float* part;          // kBack: the gate's gradient, a partial sum per 32 columns
+  const float* row_scale;  // kUp8: by token; kDown8: by row
+  const float* col_scale;
+  unsigned int* status;
+};
+
+struct Bars {
+  uint64_t *full, *empty, *acc_full, *acc_empty, *drain;
+  uint32_t* tmem_slot;
+  int* abort_flag;
+};
+
+__device__ __forceinline__ Bars bars_at(uint8_t* p) {
+  uint64_t* b = reinterpret_cast<uint64_t*>(p);
+  Bars r;
+  r.full = b;
+  r.empty = b + kMaxStages;
+  r.acc_full = b + 2 * kMaxStages;
+  r.acc_empty = r.acc_full + 2;
+  r.drain = r.acc_empty + 2;
+  r.tmem_slot = reinterpret_cast<uint32_t*>(r.drain + 1);
+  r.abort_flag = reinterpret_cast<int*>(r.tmem_slot + 1);
+  return r;
+}
+
+// One tile: rows [row, row + n) of an expert are slots, [row + n, row + padded) padding.
+struct Work {
+  int expert, row, n, padded;
+  int m0, c0;  // first channel (weights' gradients) and column
+};
+
+template <bool DW>
+__device__ __forceinline__ int work_items(const Params& p) {
+  return DW ? p.items : *p.rows.n_tiles * p.nc;
+}
+
+template <bool DW>
+__device__ __forceinline__ Work work_at(const Params& p, int w, int bn) {
+  Work k;
+  if (DW) {
+    const int e = w / (p.nm * p.nc), rest = w - e * (p.nm * p.nc);
+    k.expert = e;
+    k.row = p.rows.row_start[e];
+    k.n = k.padded = p.rows.row_start[e + 1] - k.row;
+    k.m0 = rest / p.nc * kTileRows;
+    k.c0 = rest % p.nc * bn;
+  } else {
+    const int t = w / p.nc;
+    const int4 v = p.rows.tiles[t];
+    k.expert = v.x;
+    k.row = v.y;
+    k.n = v.z;
+    k.padded = v.w;
+    k.m0 = 0;
+    k.c0 = (w - t * p.nc) * bn;
+  }
+  return k;
+}
+
+// ---- TMA producer: one warp ----------------------------------------------------------------------------------
+struct Ring {
+  RingPos pos;
+  uint32_t issued = 0;
+};
+
+// The next free stage, with `bytes` announced; null once the CTA gives up.
+template <class S>
+__device__ __forceinline__ uint8_t* next_stage(Ring& r, const Bars& b, uint8_t* smem, uint32_t bytes, int lane,
+                                               unsigned int* status) {
+  int ok = 1;
+  if (lane == 0) {
+    ok = bounded_wait(&b.empty[r.pos.i], r.pos.phase ^ 1u, b.abort_flag, status);
+    if (ok) mbar_arrive_expect_tx(&b.full[r.pos.i], bytes);
+  }
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  return ok ? smem + r.pos.i * S::kStage : nullptr;
+}
+
+// Loads still in flight when the CTA gives up must land before its shared memory is another's.
+template <class S>
+__device__ __noinline__ void settle(const Ring& r, const Bars& b) {
+  for (int i = 0; i < S::kStages; ++i) {
+    const uint32_t fills = (r.issued + S::kStages - 1 - i) / S::kStages;
+    if (fills == 0) continue;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_test_wait(&b.full[i], (fills - 1) & 1u) && global_timer_ns() - t0 < 1000000000ull) {
+    }
+  }
+}
+
+template <int MODE, int HALF>
+__device__ void producer(const Params& p, const Bars& b, uint8_t* smem, const CUtensorMap* m0, const CUtensorMap* m1,
+                         const CUtensorMap* m2, const CUtensorMap* m3) {
+  using S = Shape<MODE, HALF>;
+  const int lane = threadIdx.x & 31;
+  Ring r;
+  const int items = work_items<S::kIsDw>(p);
+  for (int w = blockIdx.x; w < items; w += gridDim.x) {
+    const Work k = work_at<S::kIsDw>(p, w, S::kBN);
+    if constexpr (S::kIsDw) {
+      // stages of 64 rows; the operand picked by token is gathered, the other one comes as boxes
+      for (int r0 = 0; r0 < k.padded; r0 += 64) {
+        const int quads = min(64, k.padded - r0) / 4;
+        const int boxes = MODE == kDwUp ? 4 : min(4, (p.cols - k.c0 + 63) / 64);
+        const uint32_t bytes = MODE == kDwUp ? 2 * kBox + 4 * quads * 512 : 2 * quads * 512 + boxes * kBox;
+        uint8_t* st = next_stage<S>(r, b, smem, bytes, lane, p.status);
+        if (!st) return settle<S>(r, b);
+        uint64_t* bar = &b.full[r.pos.i];
+        const int q = lane & 15;
+        if (q < quads) {
+          const int4 tok = *reinterpret_cast<const int4*>(p.rows.row_token + k.row + r0 + 4 * q);
+          if (MODE == kDwUp) {
+            for (int x = lane >> 4; x < 4; x += 2)
+              tma_gather4(st + kABytes + x * kBox + q * 512, m1, bar, k.c0 + 64 * x, tok);
+          } else {
+            const int x = lane >> 4;
+            tma_gather4(st + x * kBox + q * 512, m0, bar, k.m0 + 64 * x, tok);
+          }
+        }
+        if (lane == 0) {
+          if (MODE == kDwUp) {
+            tma_load_2d(st, m0, bar, k.m0, k.row + r0);
+            tma_load_2d(st + kBox, m0, bar, k.m0 + 64, k.row + r0);
+          } else {
+            for (int x = 0; x < boxes; ++x) tma_load_2d(st + kABytes + x * kBox, m1, bar, k.c0 + 64 * x, k.row + r0);
+          }
+        }
+        __syncwarp();
+        r.pos.next(S::kStages);
+        ++r.issued;
+      }
+    } else if constexpr (S::kIsUp || MODE == kBack) {
+      const int quads = k.padded / 4;
+      int4 tok = make_int4(0, 0, 0, 0);
+      if (lane < quads) tok = *reinterpret_cast<const int4*>(p.rows.row_token + k.row + 4 * lane);
+      for (int x = 0; x < p.k1; x += S::kKBlock) {
+        uint8_t* st = next_stage<S>(r, b, smem, quads * 512 + 2 * HALF * 128, lane, p.status);
+        if (!st) return settle<S>(r, b);
+        uint64_t* bar = &b.full[r.pos.i];
+        if (lane < quads) tma_gather4(st + lane * 512, m0, bar, x, tok);
+        if (lane < 2) tma_load_3d(st + kABytes + lane * HALF * 128, m1, bar, x, k.c0 + lane * p.s, k.expert);
+        __syncwarp();
+        r.pos.next(S::kStages);
+        ++r.issued;
+      }
+      if constexpr (MODE == kBack) {
+        for (int x = 0; x < p.k2; x += S::kKBlock) {
+          uint8_t* st = next_stage<S>(r, b, smem, quads * 512 + kBox, lane, p.status);
+          if (!st) return settle<S>(r, b);
+          uint64_t* bar = &b.full[r.pos.i];
+          if (lane < quads) tma_gather4(st + lane * 512, m2, bar, x, tok);
+          if (lane == 0) tma_load_3d(st + kABytes, m3, bar, k.c0, x, k.expert);
+          __syncwarp();
+          r.pos.next(S::kStages);
+          ++r.issued;
+        }
+      }
+    } else {
+      for (int x = 0; x < p.k1; x += S::kKBlock) {
+        uint8_t* st = next_stage<S>(r, b, smem, S::kStage, lane, p.status);
+        if (!st) return settle<S>(r, b);
+        uint64_t* bar = &b.full[r.pos.i];
+        if (lane == 0) {
+          tma_load_2d(st, m0, bar, x, k.row);
+          if (MODE == kDx) {
+            for (int i = 0; i < 4; ++i) tma_load_3d(st + kABytes + i * kBox, m1, bar, k.c0 + 64 * i, x, k.expert);
+          } else {
+            tma_load_3d(st + kABytes, m1, bar, x, k.c0, k.expert);
+          }
+        }
+        __syncwarp();
+        r.pos.next(S::kStages);
+        ++r.issued;
+      }
+    }
+  }
+}
+
+// ---- MMA issuer: one thread --------------------------------------------------------------------------------------
+template <int MODE, int HALF>
+__device__ void mma_role(const Params& p, const Bars& b, uint8_t* smem, uint32_t tmem) {
+  using S = Shape<MODE, HALF>;
+  RingPos s, d;
+  const uint32_t st0 = smem_u32(smem);
+  const int items = work_items<S::kIsDw>(p);
+  for (int w = blockIdx.x; w < items; w += gridDim.x) {
+    const Work k = work_at<S::kIsDw>(p, w, S::kBN);
+    if (S::kIsDw && k.padded == 0) continue;  // the epilogue writes zeros
+    if (!bounded_wait(&b.acc_empty[d.i], d.phase ^ 1u, b.abort_flag, p.status)) goto done;
+    tc_fence_after();
+    {
+      const uint32_t acc = tmem + d.i * S::kAccStride;
+      const int len1 = S::kIsDw ? k.padded : p.k1;
+      // columns of this tile's product: all, or up to the last of the weights' gradient, whole MMA steps
+      const int n = MODE == kDwDown ? min(256, (p.cols - k.c0 + 15) & ~15) : S::kIsUp || MODE == kBack ? 2 * HALF : 256;
+      for (int x = 0; x < len1; x += S::kKBlock) {
+        if (!bounded_wait(&b.full[s.i], s.phase, b.abort_flag, p.status)) goto done;
+        tc_fence_after();
+        const uint32_t a = st0 + s.i * S::kStage, bm = a + kABytes;
+        const int steps = (min(S::kKBlock, len1 - x) + S::kKStep - 1) / S::kKStep;
+        for (int i = 0; i < steps; ++i) {
+          const uint32_t more_ = (x | i) != 0;
+          if constexpr (S::kEight) {
+            mma_i8(acc, smem_desc(a + i * 32, 16, 1024, kSwizzle128B), smem_desc(bm + i * 32, 16, 1024, kSwizzle128B),
+                   idesc_s8_s32(128, n), more_);
+          } else if constexpr (S::kIsDw) {
+            mma_bf16(acc, smem_desc(a + i * 2048, kBox, 1024, kSwizzle128B),
+                     smem_desc(bm + i * 2048, kBox, 1024, kSwizzle128B), idesc_bf16_f32(128, n, 1, 1), more_);
+          } else if constexpr (MODE == kDx) {
+            mma_bf16(acc, smem_desc(a + i * 32, 16, 1024, kSwizzle128B),
+                     smem_desc(bm + i * 2048, kBox, 1024, kSwizzle128B), idesc_bf16_f32(128, n, 0, 1), more_);
+          } else {
+            mma_bf16(acc, smem_desc(a + i * 32, 16, 1024, kSwizzle128B), smem_desc(bm + i * 32, 16, 1024, kSwizzle128B),
+                     idesc_bf16_f32(128, n, 0, 0), more_);
+          }
+        }
+        mma_commit(&b.empty[s.i]);
+        s.next(S::kStages);
+      }
+      if constexpr (MODE == kBack) {
+        for (int x = 0; x < p.k2; x += S::kKBlock) {
+          if (!bounded_wait(&b.full[s.i], s.phase, b.abort_flag, p.status)) goto done;
+          tc_fence_after();
+          const uint32_t a = st0 + s.i * S::kStage, bm = a + kABytes;
+          const int steps = (min(S::kKBlock, p.k2 - x) + S::kKStep - 1) / S::kKStep;
+          for (int i = 0; i < steps; ++i)
+            mma_bf16(acc + 2 * HALF, smem_desc(a + i * 32, 16, 1024, kSwizzle128B),
+                     smem_desc(bm + i * 2048, kBox, 1024, kSwizzle128B), idesc_bf16_f32(128, HALF, 0, 1), (x | i) != 0);
+          mma_commit(&b.empty[s.i]);
+          s.next(S::kStages);
+        }
+      }
+    }
+    mma_commit(&b.acc_full[d.i]);
+    d.next(2);
+  }
+done:
+  mma_commit(b.drain);
+  bounded_wait(b.drain, 0, b.abort_flag, p.status);
+}
+
+// ---- epilogue ------------------------------------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float sigmoid(float a) { return __fdividef(1.f, 1.f + expf(-a)); }
+
+// 32 TMEM columns of this warp's lanes.
+__device__ __forceinline__ void load32(uint32_t taddr, uint32_t* v) { tmem_ld_x32(taddr, v); }
+
+template <int MODE, int HALF>
+__device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t tmem, const CUtensorMap* m_out) {
+  using S = Shape<MODE, HALF>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sp = warp & 3, hh = (warp - 4) >> 2;
+  const int t = sp * 32 + lane;  // this thread's row of the tile
+  const uint32_t lanes = (uint32_t)(sp * 32) << 16;
+  uint4* stage = reinterpret_cast<uint4*>(smem + S::kOffOut + (warp - 4) * kStageOut);
+  RingPos d;
+  const int items = work_items<S::kIsDw>(p);
+  for (int w = blockIdx.x; w < items; w += gridDim.x) {
+    const Work k = work_at<S::kIsDw>(p, w, S::kBN);
+    const bool empty = S::kIsDw && k.padded == 0;
+    const int row = k.row + t;
+    // what the rows need, read before the wait
+    float row_factor = 1.f;
+    int slot = -1;
+    if constexpr (!S::kIsDw) {
+      const bool in = t < k.padded;
+      if constexpr (MODE == kDown || MODE == kBack || MODE == kDown8) row_factor = in ? p.rows.row_gate[row] : 0.f;
+      if constexpr (MODE == kDown8) row_factor *= t < k.n ? p.row_scale[row] : 0.f;
+      if constexpr (MODE == kUp8) row_factor = in ? p.row_scale[p.rows.row_token[row]] : 0.f;
+      if constexpr (MODE == kBack) slot = in ? p.rows.row_slot[row] : -1;
+    }
+    if (!empty) {
+      if (!bounded_wait(&b.acc_full[d.i], d.phase, b.abort_flag, p.status)) break;
+      tc_fence_after();
+    }
+    const uint32_t acc = tmem + lanes + d.i * S::kAccStride;
+
+    if constexpr (S::kIsUp) {
+#pragma unroll
+      for (int c = 0; c < HALF / 2; c += 32) {
+        const int col = hh * (HALF / 2) + c;
+        uint32_t va[32], vb[32];
+        load32(acc + col, va);
+        load32(acc + HALF + col, vb);
+        tmem_wait_ld();
+        reg_fence<32>(va);
+        reg_fence<32>(vb);
+        if (c + 32 >= HALF / 2) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b.acc_empty[d.i]);
+        }
+        const int g0 = k.c0 + col;
+#pragma unroll
+        for (int q = 0; q < 32; q += 8) {
+          if (g0 + q >= p.s || t >= k.n) continue;
+          float m[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float a, u;
+            if constexpr (S::kEight) {
+              const float* sc = p.col_scale + (size_t)k.expert * 2 * p.s + g0 + q + i;
+              a = (float)(int)va[q + i] * (row_factor * __ldg(sc));
+              u = (float)(int)vb[q + i] * (row_factor * __ldg(sc + p.s));
+            } else {
+              a = __uint_as_float(va[q + i]);
+              u = __uint_as_float(vb[q + i]);
+            }
+            m[i] = a * sigmoid(a) * u;
+          }
+          if constexpr (S::kEight) {
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + (size_t)row * p.s + g0 + q);
+            o[0] = make_float4(m[0], m[1], m[2], m[3]);
+            o[1] = make_float4(m[4], m[5], m[6], m[7]);
+          } else {
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (size_t)row * p.s + g0 + q) =
+                make_uint4(pack2(m[0], m[1]), pack2(m[2], m[3]), pack2(m[4], m[5]), pack2(m[6], m[7]));
+          }
+        }
+      }
+    } else if constexpr (MODE == kBack) {
+      static_assert(MODE != kBack || HALF == 64, "32 columns a warp");
+      uint32_t va[32], vb[32], vg[32];
+      load32(acc + hh * 32, va);
+      load32(acc + HALF + hh * 32, vb);
+      load32(acc + 2 * HALF + hh * 32, vg);
+      tmem_wait_ld();
+      reg_fence<32>(va);
+      reg_fence<32>(vb);
+      reg_fence<32>(vg);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.acc_empty[d.i]);
+      const int g0 = k.c0 + hh * 32;
+      float dot = 0.f;
+      if (t < k.padded) {
+        __nv_bfloat16* pre = static_cast<__nv_bfloat16*>(p.out) + (size_t)row * 2 * p.s + g0;
+        __nv_bfloat16* mid = p.out2 + (size_t)row * p.s + g0;
+#pragma unroll
+        for (int q = 0; q < 32; q += 8) {
+          if (g0 + q >= p.s) continue;
+          float da[8], db[8], gm[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float a = __uint_as_float(va[q + i]), u = __uint_as_float(vb[q + i]);
+            const float g = __uint_as_float(vg[q + i]), sg = sigmoid(a);
+            const float m = a * sg * u, gg = row_factor * g;
+            dot = fmaf(g, m, dot);
+            // a row that is no slot contributes zeros to every gradient, whatever its token's values
+            da[i] = slot >= 0 ? gg * u * sg * (1.f + a * (1.f - sg)) : 0.f;
+            db[i] = slot >= 0 ? gg * a * sg : 0.f;
+            gm[i] = slot >= 0 ? row_factor * m : 0.f;
+          }
+          *reinterpret_cast<uint4*>(pre + q) =
+              make_uint4(pack2(da[0], da[1]), pack2(da[2], da[3]), pack2(da[4], da[5]), pack2(da[6], da[7]));
+          *reinterpret_cast<uint4*>(pre + p.s + q) =
+              make_uint4(pack2(db[0], db[1]), pack2(db[2], db[3]), pack2(db[4], db[5]), pack2(db[6], db[7]));
+          *reinterpret_cast<uint4*>(mid + q) =
+              make_uint4(pack2(gm[0], gm[1]), pack2(gm[2], gm[3]), pack2(gm[4], gm[5]), pack2(gm[6], gm[7]));
+        }
+        p.part[(size_t)(k.c0 / 32 + hh) * p.R + row] = dot;
+      }
+    } else {
+      // 64 columns at a time through the warp's own staging, 16-byte pieces placed by row so that neither side
+      // meets bank conflicts (the 128B swizzle): rows go out as whole 128-byte lines
+      const int width = min(256, p.cols - k.c0);
+#pragma unroll 1
+      for (int c = hh * 64; c < 256; c += 128) {
+        const bool last = c + 128 >= 256;
+        if (c < width) {
+          uint32_t v[64];
+          if (empty) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) v[i] = 0u;
+          } else {
+            load32(acc + c, v);
+            load32(acc + c + 32, v + 32);
+            tmem_wait_ld();
+            reg_fence<64>(v);
+          }
+          if (last && !empty) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.acc_empty[d.i]);
+          }
+          if constexpr (S::kIsDw) {
+            if (lane == 0) bulk_wait_group_read<0>();  // the last store has read the staging
+          }
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if constexpr (MODE == kDown8) {
+                const int col = k.c0 + c + q * 8 + i;
+                const float sc = col < p.cols ? __ldg(p.col_scale + (size_t)k.expert * p.cols + col) : 0.f;
+                f[i] = (float)(int)v[q * 8 + i] * (row_factor * sc);
+              } else {
+                f[i] = __uint_as_float(v[q * 8 + i]) * row_factor;
+              }
+            }
+            stage[lane * 8 + (q ^ (lane & 7))] =
+                make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+          }
+          if constexpr (S::kIsDw) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && k.m0 + sp * 32 < (MODE == kDwUp ? 2 * p.s : p.h)) {
+              tma_store_3d(m_out, stage, k.c0 + c, k.m0 + sp * 32, k.expert);
+              bulk_commit_group();
+            }
+          } else {
+            __syncwarp();
+            const int piece = lane & 7, col = k.c0 + c + piece * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int rr = i * 4 + (lane >> 3), tr = sp * 32 + rr;
+              if (tr < k.n && col < p.cols)
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (size_t)(k.row + tr) * p.cols + col) =
+                    stage[rr * 8 + (piece ^ (rr & 7))];
+            }
+            __syncwarp();
+          }
+        } else if (last && !empty) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b.acc_empty[d.i]);
+        }
+      }
+    }
+    if (!empty) d.next(2);
+  }
+  if constexpr (S::kIsDw) {
+    if (lane == 0) bulk_wait_group<0>();
+    __syncwarp();
+  }
+}
+
+template <int MODE, int HALF>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap m0, const __grid_constant__ CUtensorMap m1,
+                   const __grid_constant__ CUtensorMap m2, const __grid_constant__ CUtensorMap m3, const Params p) {
+  using S = Shape<MODE, HALF>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const Bars b = bars_at(smem + S::kOffBar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&b.full[i], 1);
+      mbar_init(&b.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b.acc_full[i], 1);
+      mbar_init(&b.acc_empty[i], kEpiWarps);
+    }
+    mbar_init(b.drain, 1);
+    *b.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(b.tmem_slot, S::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *b.tmem_slot;
+  if (warp == 0) {
+    producer<MODE, HALF>(p, b, smem, &m0, &m1, &m2, &m3);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) mma_role<MODE, HALF>(p, b, smem, tmem);
+    __syncwarp();
+  } else if (warp >= 4) {
+    epilogue<MODE, HALF>(p, b, smem, tmem, &m2);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kTmemCols);
+  }
+}
+
+// ---- host side ---------------------------------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess) {
+      f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+      fn.store(f, std::memory_order_release);
+    }
+  }
+  return f;
+}
+
+// A row-major tensor [depth][rows][width] of `bytes`-byte elements, 128B-swizzled boxes of box_w x box_h (x 1).
+bool make_map(CUtensorMap* m, const void* base, int bytes, int64_t width, int64_t rows, int64_t depth, int box_w,
+              int box_h) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint32_t rank = depth ? 3 : 2;
+  cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)depth};
+  cuuint64_t strides[2] = {(cuuint64_t)(width * bytes), (cuuint64_t)(width * rows * bytes)};
+  cuuint32_t box[3] = {(cuuint32_t)box_w, (cuuint32_t)box_h, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, rank,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, int HALF>
+cudaError_t launch(const ExpertsArgs& a, Params p, int64_t items, const CUtensorMap& m0, const CUtensorMap& m1,
+                   const CUtensorMap& m2, const CUtensorMap& m3) {
+  using S = Shape<MODE, HALF>;
+  static_assert(S::kSmem <= 227 * 1024, "shared memory");
+  int dev = 0, sms = 148;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static std::atomic<int> done[64] = {};
+  if (dev < 0 || dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(grouped_kernel<MODE, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) done[dev].store(1, std::memory_order_release);
+  }
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  p.status = a.status;
+  const int grid = (int)(items < sms ? items : sms);
+  grouped_kernel<MODE, HALF><<<grid, kThreads, S::kSmem, a.stream>>>(m0, m1, m2, m3, p);
+  return cudaGetLastError();
+}
+
+int tiles_of(int n, int bn) { return (n + bn - 1) / bn; }
+
+#define MORE_TRY(expr)                    \
+  do {                                    \
+    const cudaError_t err_ = (expr);      \
+    if (err_ != cudaSuccess) return err_; \
+  } while (0)
+#define MORE_MAP(...) \
+  if (!make_map(__VA_ARGS__)) return cudaErrorInvalidValue
+
+// H = silu(X A^T) * (X B^T); x_bytes: 2 for bf16, 1 for 8 bits
+template <int MODE>
+cudaError_t run_up(const ExpertsArgs& a, const Rows& rows, const void* X, const float* x_scale, void* H) {
+  constexpr int bytes = MODE == kUp8 ? 1 : 2, box = 128 / bytes;
+  Params p = {};
+  p.rows = rows;
+  p.k1 = a.h;
+  p.s = a.s;
+  p.h = a.h;
+  p.cols = a.s;
+  p.out = H;
+  p.row_scale = x_scale;
+  p.col_scale = a.up_scale;
+  CUtensorMap m0, m1;
+  MORE_MAP(&m0, X, bytes, a.h, a.N, 0, box, 1);
+  // 128 + 128 columns a tile; 64 + 64 where the expert has no more
+  const int half = a.s <= 64 ? 64 : 128;
+  MORE_MAP(&m1, a.W_up, bytes, a.h, 2 * (int64_t)a.s, a.M, box, half);
+  p.nc = tiles_of(a.s, half);
+  const int64_t items = max_tiles(a.S(), a.M) * p.nc;
+  if (half == 64) return launch<MODE, 64>(a, p, items, m0, m1, m0, m0);
+  return launch<MODE, 128>(a, p, items, m0, m1, m0, m0);
+}
+
+template <int MODE>
+cudaError_t run_down(const ExpertsArgs& a, const Rows& rows, const void* H, const float* h_scale, void* Y) {
+  constexpr int bytes = MODE == kDown8 ? 1 : 2, box = 128 / bytes;
+  Params p = {};
+  p.rows = rows;
+  p.k1 = a.s;
+  p.s = a.s;
+  p.h = a.h;
+  p.cols = a.h;
+  p.out = Y;
+  p.row_scale = h_scale;
+  p.col_scale = a.down_scale;
+  p.nc = tiles_of(a.h, 256);
+  CUtensorMap m0, m1;
+  MORE_MAP(&m0, H, bytes, a.s, max_rows(a.S(), a.M), 0, box, kTileRows);
+  MORE_MAP(&m1, a.W_down, bytes, a.s, a.h, a.M, box, 256);
+  return launch<MODE, 64>(a, p, max_tiles(a.S(), a.M) * p.nc, m0, m1, m0, m0);
+}
+
+}  // namespace experts
+
+using namespace experts;
+
+namespace {
+
+struct Buffers {
+  Rows rows;
+  void *H, *Hq, *Xq, *Y;
+  float *x_scale, *h_scale, *part;
+  __nv_bfloat16 *pre, *mid;
+  size_t bytes;
+};
+
+enum Kind { kForward = 0, kInt8 = 1, kBackward = 2 };
+
+int gate_parts(int s) { return (s + 63) / 64 * 2; }
+
+Buffers carve(void* scratch, int64_t N, int h, int s, int M, int k, int kind) {
+  Buffers b = {};
+  Carver c(scratch);
+  const int64_t S = N * k, R = max_rows(S, M);
+  b.rows = carve_rows(c, S, M);
+  if (kind == kForward) {
+    b.H = c.take<__nv_bfloat16>(R * s);
+  } else if (kind == kInt8) {
+    b.Xq = c.take<int8_t>(N * h);
+    b.x_scale = c.take<float>(N);
+    b.H = c.take<float>(R * s);
+    b.Hq = c.take<int8_t>(R * s);
+    b.h_scale = c.take<float>(R);
+  } else {
+    b.pre = c.take<__nv_bfloat16>(R * 2 * s);
+    b.mid = c.take<__nv_bfloat16>(R * s);
+    b.part = c.take<float>(R * gate_parts(s));
+  }
+  b.Y = c.take<__nv_bfloat16>(R * h);
+  b.bytes = c.used;
+  return b;
+}
+
+}  // namespace
+
+size_t experts_scratch(int64_t N, int h, int s, int M, int k, int kind) {
+  return carve(nullptr, N, h, s, M, k, kind).bytes;
+}
+
+cudaError_t launch_experts(const ExpertsArgs& a) {
+  const Buffers b = carve(a.scratch, a.N, a.h, a.s, a.M, a.k, kForward);
+  MORE_TRY(launch_rows(a, b.rows));
+  MORE_TRY(run_up<kUp>(a, b.rows, a.X, nullptr, b.H));
+  MORE_TRY(run_down<kDown>(a, b.rows, b.H, nullptr, b.Y));
+  return launch_combine(a, b.rows, static_cast<const __nv_bfloat16*>(b.Y), a.out);
+}
+
+cudaError_t launch_experts_int8(const ExpertsArgs& a) {
+  const Buffers b = carve(a.scratch, a.N, a.h, a.s, a.M, a.k, kInt8);
+  MORE_TRY(launch_rows(a, b.rows));
+  MORE_TRY(launch_quantize_bf16(static_cast<const __nv_bfloat16*>(a.X), a.N, a.h, static_cast<int8_t*>(b.Xq),
+                                b.x_scale, a.stream));
+  MORE_TRY(run_up<kUp8>(a, b.rows, b.Xq, b.x_scale, b.H));
+  MORE_TRY(launch_quantize_rows(a, b.rows, static_cast<const float*>(b.H), a.s, static_cast<int8_t*>(b.Hq), b.h_scale));
+  MORE_TRY(run_down<kDown8>(a, b.rows, b.Hq, b.h_scale, b.Y));
+  return launch_combine(a, b.rows, static_cast<const __nv_bfloat16*>(b.Y), a.out);
+}
+
+cudaError_t launch_experts_backward(const ExpertsArgs& a) {
+  const Buffers b = carve(a.scratch, a.N, a.h, a.s, a.M, a.k, kBackward);
+  const int64_t S = a.S(), R = max_rows(S, a.M);
+  MORE_TRY(launch_rows(a, b.rows));
+  CUtensorMap mX, mD, m1, m2, m3;
+  Params p = {};
+  p.rows = b.rows;
+  p.R = R;
+  p.s = a.s;
+  p.h = a.h;
+  MORE_MAP(&mX, a.X, 2, a.h, a.N, 0, 64, 1);
+  MORE_MAP(&mD, a.out_bar, 2, a.h, a.N, 0, 64, 1);
+  {
+    Params q = p;
+    q.k1 = q.k2 = a.h;
+    q.cols = a.s;
+    q.out = b.pre;
+    q.out2 = b.mid;
+    q.part = b.part;
+    q.nc = tiles_of(a.s, 64);
+    MORE_MAP(&m1, a.W_up, 2, a.h, 2 * (int64_t)a.s, a.M, 64, 64);
+    MORE_MAP(&m3, a.W_down, 2, a.s, a.h, a.M, 64, 64);
+    MORE_TRY((launch<kBack, 64>(a, q, max_tiles(S, a.M) * q.nc, mX, m1, mD, m3)));
+  }
+  {
+    Params q = p;
+    q.k1 = 2 * a.s;
+    q.cols = a.h;
+    q.out = b.Y;
+    q.nc = tiles_of(a.h, 256);
+    MORE_MAP(&m1, b.pre, 2, 2 * (int64_t)a.s, R, 0, 64, kTileRows);
+    MORE_MAP(&m2, a.W_up, 2, a.h, 2 * (int64_t)a.s, a.M, 64, 64);
+    MORE_TRY((launch<kDx, 64>(a, q, max_tiles(S, a.M) * q.nc, m1, m2, m1, m1)));
+  }
+  {
+    Params q = p;
+    q.cols = a.h;
+    q.nc = tiles_of(a.h, 256);
+    q.nm = tiles_of(2 * a.s, kTileRows);
+    q.items = a.M * q.nm * q.nc;
+    MORE_MAP(&m1, b.pre, 2, 2 * (int64_t)a.s, R, 0, 64, 64);
+    MORE_MAP(&m2, a.W_up_bar, 2, a.h, 2 * (int64_t)a.s, a.M, 64, 32);
+    MORE_TRY((launch<kDwUp, 64>(a, q, q.items, m1, mX, m2, m1)));
+  }
+  {
+    Params q = p;
+    q.cols = a.s;
+    q.nc = tiles_of(a.s, 256);
+    q.nm = tiles_of(a.h, kTileRows);
+    q.items = a.M * q.nm * q.nc;
+    MORE_MAP(&m1, b.mid, 2, a.s, R, 0, 64, 64);
+    MORE_MAP(&m2, a.W_down_bar, 2, a.s, a.h, a.M, 64, 32);
+    MORE_TRY((launch<kDwDown, 64>(a, q, q.items, mD, m1, m2, m1)));
+  }
+  MORE_TRY(launch_gate_grads(a, b.rows, b.part, gate_parts(a.s), R));
+  return launch_combine(a, b.rows, static_cast<const __nv_bfloat16*>(b.Y), a.out);
+}
+
+}  // namespace more
