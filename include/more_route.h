@@ -384,6 +384,28 @@ more_status more_experts_backward(const void* X, const void* W_up, const void* W
                                   float* out_gate_bar, float* out_logits_bar, void* scratch, size_t scratch_bytes,
                                   void* stream);
 
+/*
+ * The whole MoE layer (MoRE §2 "MoE layer"): more_route and then the selected experts, out = the `out` of more_experts
+ * for the router's own selections and gates.  For a few tokens (N <= 64, decoding) the experts run in one kernel that
+ * reads each selected expert's weights once and stays in fp32 up to the output; for more the call runs more_route,
+ * more_dispatch and more_experts.
+ * Arguments and requirements: those of more_route (X, R1, R2, r, k, M) and of more_experts (W_up, W_down, s, out).
+ * scratch: at least more_moe_layer_scratch_bytes(N, h, s, M, k) bytes, 16-byte aligned, one for each call that may
+ * overlap.  Asynchronous on `stream`; allocates nothing; may be captured into a graph.  The few-token kernel is a
+ * cooperative launch of one CTA per SM.
+ */
+size_t more_moe_layer_scratch_bytes(int64_t N, int h, int s, int M, int k);
+more_status more_moe_layer(const void* X, const void* R1, const void* R2, const void* W_up, const void* W_down,
+                           int64_t N, int h, int r, int s, int M, int k, void* out, void* scratch,
+                           size_t scratch_bytes, void* stream);
+
+/* more_moe_layer with the 8-bit operands of more_experts_int8 (h and s multiples of 16). */
+size_t more_moe_layer_int8_scratch_bytes(int64_t N, int h, int s, int M, int k);
+more_status more_moe_layer_int8(const void* X, const void* R1, const void* R2, const int8_t* W_up,
+                                const float* up_scale, const int8_t* W_down, const float* down_scale, int64_t N, int h,
+                                int r, int s, int M, int k, void* out, void* scratch, size_t scratch_bytes,
+                                void* stream);
+
 /* MORE_ROUTE_ABI_VERSION of the built library. */
 int more_abi_version(void);
 

@@ -23,8 +23,8 @@ from . import _build
 __all__ = ["route", "auto_variant", "route_fullrank", "selftest_wait_timeout", "route_train", "route_backward", "route_backward_scratch_bytes", "dispatch",
            "dispatch_scratch_bytes", "route_unfused", "route_unfused_tc", "route_unfused_static", "unfused_scratch_bytes", "device_status",
            "experts", "experts_scratch_bytes", "experts_backward", "experts_backward_scratch_bytes", "experts_int8",
-           "experts_int8_scratch_bytes", "quantize_rows",
-           "Router", "MoreError", "VARIANTS", "library_path", "abi_version", "KMAX", "STATS_MMAX"]
+           "experts_int8_scratch_bytes", "quantize_rows", "moe_layer", "moe_layer_scratch_bytes",
+           "moe_layer_int8", "moe_layer_int8_scratch_bytes", "Router", "MoreError", "VARIANTS", "library_path", "abi_version", "KMAX", "STATS_MMAX"]
 
 KMAX = 16
 STATS_MMAX = 32768
@@ -75,7 +75,8 @@ def _load_library() -> ctypes.CDLL:
     lib.more_route_backward.argtypes = [P, P, P, I64, I, I, I, I] + [P] * 10 + [ctypes.c_size_t, P]
     lib.more_route_unfused_scratch_bytes.restype = ctypes.c_size_t
     lib.more_route_unfused_scratch_bytes.argtypes = [I64, I, I]
-    for name in ("more_experts", "more_experts_int8", "more_experts_backward"):
+    for name in ("more_experts", "more_experts_int8", "more_experts_backward", "more_moe_layer",
+                 "more_moe_layer_int8"):
         getattr(lib, name + "_scratch_bytes").restype = ctypes.c_size_t
         getattr(lib, name + "_scratch_bytes").argtypes = [I64, I, I, I, I]
         getattr(lib, name).restype = I
@@ -83,6 +84,8 @@ def _load_library() -> ctypes.CDLL:
     lib.more_experts.argtypes = [P, P, P, I64, I, I, I, I, P, P, P, P] + tail
     lib.more_experts_int8.argtypes = [P, P, P, P, P, I64, I, I, I, I, P, P, P, P] + tail
     lib.more_experts_backward.argtypes = [P, P, P, I64, I, I, I, I] + [P] * 9 + tail
+    lib.more_moe_layer.argtypes = [P, P, P, P, P, I64, I, I, I, I, I, P] + tail
+    lib.more_moe_layer_int8.argtypes = [P, P, P, P, P, P, P, I64, I, I, I, I, I, P] + tail
     lib.more_quantize_rows.restype = I
     lib.more_quantize_rows.argtypes = [P, I64, I, P, P, P]
     lib.more_device_status.restype = I
@@ -416,6 +419,60 @@ def experts_backward(X: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tensor, 
                                         scratch.numel(), _stream_handle(stream))
     _check(st, "more_experts_backward")
     return outs
+
+
+def moe_layer_scratch_bytes(N: int, h: int, s: int, M: int, k: int) -> int:
+    return int(_lib.more_moe_layer_scratch_bytes(N, h, s, M, k))
+
+
+def moe_layer_int8_scratch_bytes(N: int, h: int, s: int, M: int, k: int) -> int:
+    return int(_lib.more_moe_layer_int8_scratch_bytes(N, h, s, M, k))
+
+
+def _layer_shapes(X, R1, R2, W_up, W_down, dtype):
+    if X.dim() != 2 or R1.dim() != 2 or R2.dim() != 2 or W_up.dim() != 3 or W_down.dim() != 3:
+        raise ValueError("X, R1 and R2 are matrices, W_up and W_down one matrix per expert")
+    N, h = _as_bf16(X, "X").shape
+    r, M = _as_bf16(R2, "R2").shape
+    s = W_down.shape[2]
+    _typed(R1, "R1", torch.bfloat16, (h, r))
+    _typed(W_up, "W_up", dtype, (M, 2 * s, h))
+    _typed(W_down, "W_down", dtype, (M, h, s))
+    return N, h, r, s, M
+
+
+def moe_layer(X: torch.Tensor, R1: torch.Tensor, R2: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tensor, k: int, *,
+              out=None, scratch: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The whole layer: :func:`route` and the selected :func:`experts`, for a few tokens (N <= 64) the experts in one
+    kernel.  Weights as for :func:`experts`.  Returns bf16 [N, h]."""
+    N, h, r, s, M = _layer_shapes(X, R1, R2, W_up, W_down, torch.bfloat16)
+    device, stream = _on_device(X, stream, R1=R1, R2=R2, W_up=W_up, W_down=W_down, out=out, scratch=scratch)
+    with device, torch.cuda.stream(stream):
+        out = _output(out, "out", torch.bfloat16, (N, h), X.device)
+        scratch = _scratch(scratch, moe_layer_scratch_bytes(N, h, s, M, k), X.device)
+        st = _lib.more_moe_layer(_ptr(X), _ptr(R1), _ptr(R2), _ptr(W_up), _ptr(W_down), N, h, r, s, M, k, _ptr(out),
+                                 _ptr(scratch), scratch.numel(), _stream_handle(stream))
+    _check(st, "more_moe_layer")
+    return out
+
+
+def moe_layer_int8(X: torch.Tensor, R1: torch.Tensor, R2: torch.Tensor, W_up: torch.Tensor, up_scale: torch.Tensor,
+                   W_down: torch.Tensor, down_scale: torch.Tensor, k: int, *, out=None,
+                   scratch: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """:func:`moe_layer` with the 8-bit operands of :func:`experts_int8`."""
+    N, h, r, s, M = _layer_shapes(X, R1, R2, W_up, W_down, torch.int8)
+    _typed(up_scale, "up_scale", torch.float32, (M, 2 * s))
+    _typed(down_scale, "down_scale", torch.float32, (M, h))
+    device, stream = _on_device(X, stream, R1=R1, R2=R2, W_up=W_up, up_scale=up_scale, W_down=W_down,
+                                down_scale=down_scale, out=out, scratch=scratch)
+    with device, torch.cuda.stream(stream):
+        out = _output(out, "out", torch.bfloat16, (N, h), X.device)
+        scratch = _scratch(scratch, moe_layer_int8_scratch_bytes(N, h, s, M, k), X.device)
+        st = _lib.more_moe_layer_int8(_ptr(X), _ptr(R1), _ptr(R2), _ptr(W_up), _ptr(up_scale), _ptr(W_down),
+                                      _ptr(down_scale), N, h, r, s, M, k, _ptr(out), _ptr(scratch), scratch.numel(),
+                                      _stream_handle(stream))
+    _check(st, "more_moe_layer_int8")
+    return out
 
 
 def auto_variant(N: int, h: int, r: int, M: int, k: int) -> str | None:

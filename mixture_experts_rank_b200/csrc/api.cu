@@ -500,6 +500,150 @@ more_status more_experts_backward(const void* X, const void* W_up, const void* W
   return launch_experts_backward(a) == cudaSuccess ? MORE_OK : MORE_ERR_CUDA;
 }
 
+}  // extern "C"
+
+namespace more {
+namespace {
+
+// Scratch of a whole-layer call: what the router leaves, then either the few-token kernel's buffers or those of
+// dispatch and the grouped products.
+struct LayerBuffers {
+  int32_t *idx, *counts, *offsets, *slots;
+  float *gate, *mid, *x_scale;
+  int8_t* Xq;
+  unsigned int* barrier;
+  void *dispatch, *experts;
+  size_t dispatch_bytes, experts_bytes, bytes;
+};
+
+LayerBuffers carve_layer(void* scratch, int64_t N, int h, int s, int M, int k, bool int8) {
+  LayerBuffers b = {};
+  Carver c(scratch);
+  const int64_t S = N * k;
+  b.idx = c.take<int32_t>(S);
+  b.gate = c.take<float>(S);
+  b.counts = c.take<int32_t>((int64_t)M + 64);  // the barrier's counter follows the counts: one memset for both
+  if (layer_few_fits(N, h, k)) {
+    b.barrier = b.counts ? reinterpret_cast<unsigned int*>(b.counts) + (M + 31) / 32 * 32 : nullptr;
+    b.mid = c.take<float>(S * s);
+    if (int8) {
+      b.Xq = c.take<int8_t>(N * h);
+      b.x_scale = c.take<float>(N);
+    }
+  } else {
+    b.offsets = c.take<int32_t>((int64_t)M + 1);
+    b.slots = c.take<int32_t>(S);
+    b.dispatch_bytes = (size_t)dispatch_scratch_bytes(S, M);
+    b.dispatch = c.take<uint8_t>((int64_t)b.dispatch_bytes);
+    b.experts_bytes = experts_scratch(N, h, s, M, k, int8 ? 1 : 0);
+    b.experts = c.take<uint8_t>((int64_t)b.experts_bytes);
+  }
+  b.bytes = c.used;
+  return b;
+}
+
+size_t layer_scratch_checked(int64_t N, int h, int s, int M, int k, bool int8) {
+  if (N < 0 || h < 1 || s < 1 || M < 1 || k < 1 || !experts_supported(N, h, s, M, k)) return 0;
+  return carve_layer(nullptr, N, h, s, M, k, int8).bytes;
+}
+
+more_status moe_layer(const void* X, const void* R1, const void* R2, const void* W_up, const float* up_scale,
+                      const void* W_down, const float* down_scale, int64_t N, int h, int r, int s, int M, int k,
+                      void* out, void* scratch, size_t scratch_bytes, cudaStream_t stream) {
+  const bool int8 = up_scale != nullptr;
+  const LayerBuffers b = carve_layer(scratch, N, h, s, M, k, int8);
+  if (scratch_bytes < b.bytes) return MORE_ERR_INVALID_ARG;
+  unsigned int* status = status_word();
+  if (!status) return MORE_ERR_CUDA;
+  if (!layer_few_fits(N, h, k)) {
+    more_status st = more_route(X, R1, R2, N, h, r, M, k, b.idx, b.gate, b.counts, nullptr, stream);
+    if (st == MORE_OK)
+      st = more_dispatch(b.idx, N, k, M, b.offsets, b.slots, b.dispatch, b.dispatch_bytes, stream);
+    if (st != MORE_OK) return st;
+    return int8 ? more_experts_int8(X, static_cast<const int8_t*>(W_up), up_scale, static_cast<const int8_t*>(W_down),
+                                    down_scale, N, h, s, M, k, b.gate, b.offsets, b.slots, out, b.experts,
+                                    b.experts_bytes, stream)
+                : more_experts(X, W_up, W_down, N, h, s, M, k, b.gate, b.offsets, b.slots, out, b.experts,
+                               b.experts_bytes, stream);
+  }
+  RouteArgs a = make_args(X, R1, R2, N, h, r, M, k, b.idx, b.gate, b.counts, nullptr, stream);
+  a.status = status;
+  FewArgs f = {};
+  f.X = X;
+  f.W_up = W_up;
+  f.W_down = W_down;
+  f.up_scale = up_scale;
+  f.down_scale = down_scale;
+  f.idx = b.idx;
+  f.gate = b.gate;
+  f.mid = b.mid;
+  f.barrier = b.barrier;
+  f.out = out;
+  f.N = N;
+  f.h = h;
+  f.s = s;
+  f.M = M;
+  f.k = k;
+  f.status = status;
+  f.stream = stream;
+  cudaError_t e = cudaMemsetAsync(b.counts, 0, sizeof(int32_t) * ((size_t)M + 64), stream);
+  if (e == cudaSuccess && int8) {
+    f.Xq = b.Xq;
+    f.x_scale = b.x_scale;
+    e = launch_quantize_bf16(static_cast<const __nv_bfloat16*>(X), N, h, b.Xq, b.x_scale, stream);
+  }
+  if (e == cudaSuccess) e = auto_variant(a) == MORE_VARIANT_CLUSTER ? launch_cluster(a) : launch_small_n(a);
+  if (e == cudaSuccess) e = launch_layer_few(f);
+  return e == cudaSuccess ? MORE_OK : MORE_ERR_CUDA;
+}
+
+more_status validate_layer(const void* X, const void* R1, const void* R2, const void* W_up, const float* up_scale,
+                           const void* W_down, const float* down_scale, int64_t N, int h, int r, int s, int M, int k,
+                           const void* out, const void* scratch, int unit) {
+  const more_status st = validate_shape(N, h, r, M, k);
+  if (st == MORE_ERR_INVALID_ARG || h % unit || s < unit || s % unit) return MORE_ERR_INVALID_ARG;
+  if (!R1 || !R2 || !W_up || !W_down || (unit == 16 && (!up_scale || !down_scale)) ||
+      (N > 0 && (!X || !out || !scratch)))
+    return MORE_ERR_INVALID_ARG;
+  for (const void* p : {X, R1, R2, W_up, (const void*)up_scale, W_down, (const void*)down_scale, out, scratch})
+    if (p && !aligned16(p)) return MORE_ERR_INVALID_ARG;
+  if (st != MORE_OK) return st;
+  return experts_supported(N, h, s, M, k) ? MORE_OK : MORE_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+}  // namespace more
+
+extern "C" {
+
+size_t more_moe_layer_scratch_bytes(int64_t N, int h, int s, int M, int k) {
+  return layer_scratch_checked(N, h, s, M, k, false);
+}
+
+more_status more_moe_layer(const void* X, const void* R1, const void* R2, const void* W_up, const void* W_down,
+                           int64_t N, int h, int r, int s, int M, int k, void* out, void* scratch,
+                           size_t scratch_bytes, void* stream) {
+  const more_status st = validate_layer(X, R1, R2, W_up, nullptr, W_down, nullptr, N, h, r, s, M, k, out, scratch, 8);
+  if (st != MORE_OK || N == 0) return st;
+  return moe_layer(X, R1, R2, W_up, nullptr, W_down, nullptr, N, h, r, s, M, k, out, scratch, scratch_bytes,
+                   static_cast<cudaStream_t>(stream));
+}
+
+size_t more_moe_layer_int8_scratch_bytes(int64_t N, int h, int s, int M, int k) {
+  return layer_scratch_checked(N, h, s, M, k, true);
+}
+
+more_status more_moe_layer_int8(const void* X, const void* R1, const void* R2, const int8_t* W_up,
+                                const float* up_scale, const int8_t* W_down, const float* down_scale, int64_t N, int h,
+                                int r, int s, int M, int k, void* out, void* scratch, size_t scratch_bytes,
+                                void* stream) {
+  const more_status st =
+      validate_layer(X, R1, R2, W_up, up_scale, W_down, down_scale, N, h, r, s, M, k, out, scratch, 16);
+  if (st != MORE_OK || N == 0) return st;
+  return moe_layer(X, R1, R2, W_up, up_scale, W_down, down_scale, N, h, r, s, M, k, out, scratch, scratch_bytes,
+                   static_cast<cudaStream_t>(stream));
+}
+
 more_status more_selftest_wait_timeout(int32_t* out_result, void* stream) {
   if (!out_result || (reinterpret_cast<uintptr_t>(out_result) & 3u)) return MORE_ERR_INVALID_ARG;
   unsigned int* status = status_word();

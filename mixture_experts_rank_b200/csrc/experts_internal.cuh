@@ -105,6 +105,26 @@ cudaError_t launch_quantize_bf16(const __nv_bfloat16* v, int64_t rows, int width
 cudaError_t launch_quantize_rows(const ExpertsArgs& a, const Rows& r, const float* v, int width, int8_t* q,
                                  float* scale);
 
+// The selected experts of a few tokens (moe_layer.cu).  Xq and the scales: 8-bit weights.
+struct FewArgs {
+  const void* X;
+  const int8_t* Xq;
+  const float* x_scale;
+  const void *W_up, *W_down;
+  const float *up_scale, *down_scale;
+  const int32_t* idx;
+  const float* gate;
+  float* mid;             // [N k][s]
+  unsigned int* barrier;  // zeroed before the launch
+  void* out;
+  int64_t N;
+  int h, s, M, k;
+  unsigned int* status;
+  cudaStream_t stream;
+};
+bool layer_few_fits(int64_t N, int h, int k);
+cudaError_t launch_layer_few(const FewArgs& f);
+
 size_t experts_scratch(int64_t N, int h, int s, int M, int k, int kind);  // kind: 0 bf16, 1 int8, 2 backward
 cudaError_t launch_experts(const ExpertsArgs& a);
 cudaError_t launch_experts_int8(const ExpertsArgs& a);

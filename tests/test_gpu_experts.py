@@ -117,3 +117,47 @@ def test_experts_backward(size, how):
     want, bound = ref.backward(**args, out_bar=out_bar)
     for name, t in zip(("X_bar", "W_up_bar", "W_down_bar", "gate_bar", "logits_bar"), got):
         ref.check(t, want[name], bound[name], name)
+
+
+LAYERS = [  # N, h, r, s, M, k: few tokens on one kernel, then more than it takes
+    (1, 16, 16, 16, 8, 1), (1, 2048, 32, 64, 256, 8), (2, 64, 16, 16, 8, 8), (13, 1040, 64, 352, 64, 6),
+    (64, 128, 32, 48, 16, 16), (33, 4112, 128, 32, 24, 2), (64, 256, 32, 1040, 8, 2), (5, 320, 16, 2064, 16, 3),
+    (65, 128, 32, 48, 16, 4), (300, 256, 32, 80, 64, 8),
+]
+
+
+def layer_inputs(N, h, r, s, M, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return dict(X=rnd(g, N, h), R1=rnd(g, h, r, scale=h**-0.5), R2=rnd(g, r, M, scale=r**-0.5),
+                W_up=rnd(g, M, 2 * s, h, scale=h**-0.5), W_down=rnd(g, M, h, s, scale=s**-0.5))
+
+
+def layer_reference(args, k, fp32_rows, **scales):
+    """The experts in 64 bits for the router's own selections and gates."""
+    import mixture_experts_rank_b200 as more
+    idx, gate, _, _ = more.route(args["X"], args["R1"], args["R2"], k)
+    offsets, slots = more.dispatch(idx, args["W_down"].shape[0])
+    return ref.forward(args["X"], args["W_up"], args["W_down"], gate, offsets, slots, fp32_rows=fp32_rows, **scales)
+
+
+@pytest.mark.parametrize("size", LAYERS, ids=str)
+def test_moe_layer(size):
+    import mixture_experts_rank_b200 as more
+    N, h, r, s, M, k = size
+    args = layer_inputs(N, h, r, s, M)
+    out, untouched = guarded((N, h), torch.bfloat16)
+    more.moe_layer(**args, k=k, out=out)
+    assert ok() and untouched()
+    ref.check(out, *layer_reference(args, k, N <= 64), "out")
+
+
+@pytest.mark.parametrize("size", LAYERS, ids=str)
+def test_moe_layer_int8(size):
+    import mixture_experts_rank_b200 as more
+    N, h, r, s, M, k = size
+    args = int8_of(layer_inputs(N, h, r, s, M))
+    out, untouched = guarded((N, h), torch.bfloat16)
+    more.moe_layer_int8(**args, k=k, out=out)
+    assert ok() and untouched()
+    scales = {n: args[n] for n in ("up_scale", "down_scale")}
+    ref.check(out, *layer_reference(args, k, N <= 64, **scales), "out")
