@@ -13,8 +13,8 @@
 //
 // A CTA holds 128 rows of one expert (128 output channels for the weights' gradients) on the TMEM lanes and up
 // to 256 columns:
-//   warp 0       TMA: stages of 128 bytes of K (64 values of 16 bits, 128 of 8), 128B-swizzled; rows that are
-//                picked by token come by gathered loads, one quad of rows a lane;
+//   warp 0       TMA: stages of 128 bytes of K (64 values of 16 bits, 128 of 8), 128B-swizzled;
+//   warps 12-15  asynchronous copies of the rows that are picked by token;
 //   warp 1       tcgen05 MMAs into two accumulators in TMEM, so a tile's epilogue runs under the next one's products;
 //   warps 4-11   epilogue, two warps a lane group.
 // The grid is persistent; tiles come from the row layout that the same call made on the device.
@@ -35,8 +35,9 @@ using namespace sm100;
 
 enum Mode { kUp, kDown, kUp8, kDown8, kBack, kDx, kDwUp, kDwDown };
 
-constexpr int kThreads = 12 * 32;
+constexpr int kThreads = 16 * 32;
 constexpr int kEpiWarps = 8;
+constexpr int kGatherWarps = 4;
 constexpr uint32_t kABytes = kTileRows * 128;  // 16 KB: 128 rows (or 2 boxes of 64 channels x 64 rows) of a stage
 constexpr uint32_t kBox = 64 * 128;            // 8 KB: a box of 64 rows x 128 bytes
 constexpr uint32_t kStageOut = 32 * 128;       // a warp's staging: 32 rows x 64 bf16 columns
@@ -48,6 +49,7 @@ struct Shape {
   static constexpr bool kIsUp = MODE == kUp || MODE == kUp8;
   static constexpr bool kIsDown = MODE == kDown || MODE == kDown8;
   static constexpr bool kIsDw = MODE == kDwUp || MODE == kDwDown;
+  static constexpr bool kGathers = kIsUp || kIsDw || MODE == kBack;  // one operand is picked by token
   static constexpr bool kStaged = kIsDown || MODE == kDx || kIsDw;  // epilogue goes through shared memory
   // columns of one accumulator, and its place in TMEM
   static constexpr int kCols = kIsUp ? 2 * HALF : MODE == kBack ? 3 * HALF : 256;
@@ -73,6 +75,8 @@ struct Params {
   int k1, k2;     // contracted lengths (k2: the second product of kBack)
   int s, h;
   int cols;       // output columns
+  const void* X;        // the rows picked by token, and kBack's second set
+  const void* out_bar;
   void* out;      // kUp: H; kUp8: H in fp32; kDown, kDx: rows of h; kBack: [da, db]
   __nv_bfloat16* out2;  // kBack: gate * m
   float* part;          // kBack: the gate's gradient, a partial sum per 32 columns
@@ -134,26 +138,29 @@ __device__ __forceinline__ Work work_at(const Params& p, int w, int bn) {
   return k;
 }
 
-// ---- TMA producer: one warp ----------------------------------------------------------------------------------
+// ---- loads -----------------------------------------------------------------------------------------------------
+// Warp 0 issues the operands that come as boxes; kGatherWarps warps copy the rows that are picked by token, 16 bytes a
+// lane, four rows of 128 bytes an instruction, placed as the 128B swizzle places them.  (Gathered TMA loads move no more
+// than 3.4 TB/s over the machine however many warps issue them; these copies are not bound by their issue.)
+// Every one of these warps waits for every stage and arrives on it.
 struct Ring {
   RingPos pos;
   uint32_t issued = 0;
+  template <class S>
+  __device__ __forceinline__ void next() {
+    pos.next(S::kStages);
+    ++issued;
+  }
 };
 
-// The next free stage, with `bytes` announced; null once the CTA gives up.
 template <class S>
-__device__ __forceinline__ uint8_t* next_stage(Ring& r, const Bars& b, uint8_t* smem, uint32_t bytes, int lane,
-                                               unsigned int* status) {
+__device__ __forceinline__ bool wait_empty(const Ring& r, const Bars& b, int lane, unsigned int* status) {
   int ok = 1;
-  if (lane == 0) {
-    ok = bounded_wait(&b.empty[r.pos.i], r.pos.phase ^ 1u, b.abort_flag, status);
-    if (ok) mbar_arrive_expect_tx(&b.full[r.pos.i], bytes);
-  }
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  return ok ? smem + r.pos.i * S::kStage : nullptr;
+  if (lane == 0) ok = bounded_wait(&b.empty[r.pos.i], r.pos.phase ^ 1u, b.abort_flag, status);
+  return __shfl_sync(0xffffffffu, ok, 0);
 }
 
-// Loads still in flight when the CTA gives up must land before its shared memory is another's.
+// Box loads still in flight when the CTA gives up must land before its shared memory is another's.
 template <class S>
 __device__ __noinline__ void settle(const Ring& r, const Bars& b) {
   for (int i = 0; i < S::kStages; ++i) {
@@ -166,91 +173,144 @@ __device__ __noinline__ void settle(const Ring& r, const Bars& b) {
 }
 
 template <int MODE, int HALF>
-__device__ void producer(const Params& p, const Bars& b, uint8_t* smem, const CUtensorMap* m0, const CUtensorMap* m1,
-                         const CUtensorMap* m2, const CUtensorMap* m3) {
+__device__ void box_loads(const Params& p, const Bars& b, uint8_t* smem, const CUtensorMap* m0, const CUtensorMap* m1,
+                          const CUtensorMap* m3) {
   using S = Shape<MODE, HALF>;
   const int lane = threadIdx.x & 31;
   Ring r;
   const int items = work_items<S::kIsDw>(p);
   for (int w = blockIdx.x; w < items; w += gridDim.x) {
     const Work k = work_at<S::kIsDw>(p, w, S::kBN);
-    if constexpr (S::kIsDw) {
-      // stages of 64 rows; the operand picked by token is gathered, the other one comes as boxes
-      for (int r0 = 0; r0 < k.padded; r0 += 64) {
-        const int quads = min(64, k.padded - r0) / 4;
-        const int boxes = MODE == kDwUp ? 4 : min(4, (p.cols - k.c0 + 63) / 64);
-        const uint32_t bytes = MODE == kDwUp ? 2 * kBox + 4 * quads * 512 : 2 * quads * 512 + boxes * kBox;
-        uint8_t* st = next_stage<S>(r, b, smem, bytes, lane, p.status);
-        if (!st) return settle<S>(r, b);
+    const int len = S::kIsDw ? k.padded : p.k1 + (MODE == kBack ? (p.k1 + 63) / 64 * 64 - p.k1 + p.k2 : 0);
+    for (int x = 0; x < len; x += S::kKBlock) {
+      if (!wait_empty<S>(r, b, lane, p.status)) return settle<S>(r, b);
+      if (lane == 0) {
         uint64_t* bar = &b.full[r.pos.i];
-        const int q = lane & 15;
-        if (q < quads) {
-          const int4 tok = *reinterpret_cast<const int4*>(p.rows.row_token + k.row + r0 + 4 * q);
-          if (MODE == kDwUp) {
-            for (int x = lane >> 4; x < 4; x += 2)
-              tma_gather4(st + kABytes + x * kBox + q * 512, m1, bar, k.c0 + 64 * x, tok);
+        uint8_t* st = smem + r.pos.i * S::kStage;
+        if constexpr (MODE == kDwUp) {
+          mbar_arrive_expect_tx(bar, 2 * kBox);
+          tma_load_2d(st, m0, bar, k.m0, k.row + x);
+          tma_load_2d(st + kBox, m0, bar, k.m0 + 64, k.row + x);
+        } else if constexpr (MODE == kDwDown) {
+          const int boxes = min(4, (p.cols - k.c0 + 63) / 64);
+          mbar_arrive_expect_tx(bar, boxes * kBox);
+          for (int i = 0; i < boxes; ++i) tma_load_2d(st + kABytes + i * kBox, m1, bar, k.c0 + 64 * i, k.row + x);
+        } else if constexpr (S::kIsUp || MODE == kBack) {
+          if (x < p.k1) {
+            mbar_arrive_expect_tx(bar, 2 * HALF * 128);
+            tma_load_3d(st + kABytes, m1, bar, x, k.c0, k.expert);
+            tma_load_3d(st + kABytes + HALF * 128, m1, bar, x, k.c0 + p.s, k.expert);
           } else {
-            const int x = lane >> 4;
-            tma_gather4(st + x * kBox + q * 512, m0, bar, k.m0 + 64 * x, tok);
+            mbar_arrive_expect_tx(bar, kBox);
+            tma_load_3d(st + kABytes, m3, bar, k.c0, x - (p.k1 + 63) / 64 * 64, k.expert);
           }
-        }
-        if (lane == 0) {
-          if (MODE == kDwUp) {
-            tma_load_2d(st, m0, bar, k.m0, k.row + r0);
-            tma_load_2d(st + kBox, m0, bar, k.m0 + 64, k.row + r0);
-          } else {
-            for (int x = 0; x < boxes; ++x) tma_load_2d(st + kABytes + x * kBox, m1, bar, k.c0 + 64 * x, k.row + r0);
-          }
-        }
-        __syncwarp();
-        r.pos.next(S::kStages);
-        ++r.issued;
-      }
-    } else if constexpr (S::kIsUp || MODE == kBack) {
-      const int quads = k.padded / 4;
-      int4 tok = make_int4(0, 0, 0, 0);
-      if (lane < quads) tok = *reinterpret_cast<const int4*>(p.rows.row_token + k.row + 4 * lane);
-      for (int x = 0; x < p.k1; x += S::kKBlock) {
-        uint8_t* st = next_stage<S>(r, b, smem, quads * 512 + 2 * HALF * 128, lane, p.status);
-        if (!st) return settle<S>(r, b);
-        uint64_t* bar = &b.full[r.pos.i];
-        if (lane < quads) tma_gather4(st + lane * 512, m0, bar, x, tok);
-        if (lane < 2) tma_load_3d(st + kABytes + lane * HALF * 128, m1, bar, x, k.c0 + lane * p.s, k.expert);
-        __syncwarp();
-        r.pos.next(S::kStages);
-        ++r.issued;
-      }
-      if constexpr (MODE == kBack) {
-        for (int x = 0; x < p.k2; x += S::kKBlock) {
-          uint8_t* st = next_stage<S>(r, b, smem, quads * 512 + kBox, lane, p.status);
-          if (!st) return settle<S>(r, b);
-          uint64_t* bar = &b.full[r.pos.i];
-          if (lane < quads) tma_gather4(st + lane * 512, m2, bar, x, tok);
-          if (lane == 0) tma_load_3d(st + kABytes, m3, bar, k.c0, x, k.expert);
-          __syncwarp();
-          r.pos.next(S::kStages);
-          ++r.issued;
-        }
-      }
-    } else {
-      for (int x = 0; x < p.k1; x += S::kKBlock) {
-        uint8_t* st = next_stage<S>(r, b, smem, S::kStage, lane, p.status);
-        if (!st) return settle<S>(r, b);
-        uint64_t* bar = &b.full[r.pos.i];
-        if (lane == 0) {
+        } else {
+          mbar_arrive_expect_tx(bar, S::kStage);
           tma_load_2d(st, m0, bar, x, k.row);
-          if (MODE == kDx) {
+          if constexpr (MODE == kDx) {
             for (int i = 0; i < 4; ++i) tma_load_3d(st + kABytes + i * kBox, m1, bar, k.c0 + 64 * i, x, k.expert);
           } else {
             tma_load_3d(st + kABytes, m1, bar, x, k.c0, k.expert);
           }
         }
-        __syncwarp();
-        r.pos.next(S::kStages);
-        ++r.issued;
+      }
+      __syncwarp();
+      r.next<S>();
+    }
+  }
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+
+// This lane's arrival on a stage, made once its copies so far have landed.  The copies are generic-proxy writes: the
+// MMA thread orders its own reads behind them with a proxy fence after its wait.  (The same fence on this side waits
+// for every copy in flight and leaves one stage of them at a time: the 8-bit first product took 331 instead of 203 us.)
+__device__ __forceinline__ void arrive_landed(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+template <int MODE, int HALF>
+__device__ void row_copies(const Params& p, const Bars& b, uint8_t* smem, int turn) {
+  using S = Shape<MODE, HALF>;
+  const int lane = threadIdx.x & 31, sub = lane >> 3, piece = lane & 7;
+  const size_t pitch = (size_t)p.h * (S::kEight ? 1 : 2);
+  const uint32_t st0 = smem_u32(smem);
+  Ring c;
+  const int items = work_items<S::kIsDw>(p);
+  for (int w = blockIdx.x; w < items; w += gridDim.x) {
+    const Work k = work_at<S::kIsDw>(p, w, S::kBN);
+    if constexpr (S::kIsDw) {
+      // stages of 64 rows; boxes of 64 columns: two of y_bar as A, four of x as B
+      constexpr int kBoxes = MODE == kDwUp ? 4 : 2;
+      const uint8_t* src = static_cast<const uint8_t*>(MODE == kDwUp ? p.X : p.out_bar);
+      const int col = MODE == kDwUp ? k.c0 : k.m0;
+      const int32_t* tokens = p.rows.row_token + k.row + sub;
+      int tok[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tok[i] = 4 * (turn + 4 * i) < k.padded ? tokens[4 * (turn + 4 * i)] : 0;
+      for (int r0 = 0; r0 < k.padded; r0 += 64) {
+        int next[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int q = r0 + 64 + 4 * (turn + 4 * i);
+          next[i] = q < k.padded ? tokens[q] : 0;
+        }
+        if (!wait_empty<S>(c, b, lane, p.status)) return wait_copies();
+        const uint32_t st = st0 + c.pos.i * S::kStage + (MODE == kDwUp ? kABytes : 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 4 * (turn + 4 * i) + sub;
+          if (r0 + row >= k.padded) continue;
+          const uint32_t dst = st + row * 128 + ((piece ^ (row & 7)) << 4);
+#pragma unroll
+          for (int x = 0; x < kBoxes; ++x) {
+            const int cc = col + 64 * x + piece * 8;
+            const bool ok = cc < p.h;
+            copy16(dst + x * kBox, src + (size_t)tok[i] * pitch + (ok ? 2 * cc : 0), ok);
+          }
+        }
+        arrive_landed(&b.full[c.pos.i]);
+        c.next<S>();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tok[i] = next[i];
+      }
+    } else {
+      const uint8_t* row[8];
+      uint32_t at[8];
+      const uint8_t* X = static_cast<const uint8_t*>(p.X);
+      size_t tok[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = 4 * (turn + 4 * i) + sub;
+        tok[i] = r < k.padded ? p.rows.row_token[k.row + r] : 0;
+        row[i] = X + tok[i] * pitch + piece * 16;
+        at[i] = r * 128 + ((piece ^ (r & 7)) << 4);
+      }
+      const int passes = MODE == kBack ? 2 : 1;
+      for (int pass = 0; pass < passes; ++pass) {
+        if (pass == 1) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            row[i] = static_cast<const uint8_t*>(p.out_bar) + tok[i] * pitch + piece * 16;
+        }
+        for (int x = 0; x < (int)pitch; x += 128) {
+          if (!wait_empty<S>(c, b, lane, p.status)) return wait_copies();
+          const uint32_t st = st0 + c.pos.i * S::kStage;
+          const bool ok = x + piece * 16 < (int)pitch;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (4 * (turn + 4 * i) < k.padded) copy16(st + at[i], row[i] + (ok ? x : 0) - (ok ? 0 : piece * 16), ok);
+          arrive_landed(&b.full[c.pos.i]);
+        c.next<S>();
+        }
       }
     }
   }
+  wait_copies();
 }
 
 // ---- MMA issuer: one thread --------------------------------------------------------------------------------------
@@ -272,6 +332,7 @@ __device__ void mma_role(const Params& p, const Bars& b, uint8_t* smem, uint32_t
       const int n = MODE == kDwDown ? min(256, (p.cols - k.c0 + 15) & ~15) : S::kIsUp || MODE == kBack ? 2 * HALF : 256;
       for (int x = 0; x < len1; x += S::kKBlock) {
         if (!bounded_wait(&b.full[s.i], s.phase, b.abort_flag, p.status)) goto done;
+        if constexpr (S::kGathers) fence_proxy_async_smem();
         tc_fence_after();
         const uint32_t a = st0 + s.i * S::kStage, bm = a + kABytes;
         const int steps = (min(S::kKBlock, len1 - x) + S::kKStep - 1) / S::kKStep;
@@ -297,6 +358,7 @@ __device__ void mma_role(const Params& p, const Bars& b, uint8_t* smem, uint32_t
       if constexpr (MODE == kBack) {
         for (int x = 0; x < p.k2; x += S::kKBlock) {
           if (!bounded_wait(&b.full[s.i], s.phase, b.abort_flag, p.status)) goto done;
+          fence_proxy_async_smem();
           tc_fence_after();
           const uint32_t a = st0 + s.i * S::kStage, bm = a + kABytes;
           const int steps = (min(S::kKBlock, p.k2 - x) + S::kKStep - 1) / S::kKStep;
@@ -530,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(&b.full[i], 1);
+      mbar_init(&b.full[i], 1 + (S::kGathers ? kGatherWarps * 32 : 0));
       mbar_init(&b.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -550,10 +612,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *b.tmem_slot;
   if (warp == 0) {
-    producer<MODE, HALF>(p, b, smem, &m0, &m1, &m2, &m3);
+    box_loads<MODE, HALF>(p, b, smem, &m0, &m1, &m3);
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) mma_role<MODE, HALF>(p, b, smem, tmem);
+    __syncwarp();
+  } else if (warp >= 12) {
+    if constexpr (S::kGathers) row_copies<MODE, HALF>(p, b, smem, warp - 12);
     __syncwarp();
   } else if (warp >= 4) {
     epilogue<MODE, HALF>(p, b, smem, tmem, &m2);
@@ -642,15 +707,15 @@ cudaError_t run_up(const ExpertsArgs& a, const Rows& rows, const void* X, const 
   p.out = H;
   p.row_scale = x_scale;
   p.col_scale = a.up_scale;
-  CUtensorMap m0, m1;
-  MORE_MAP(&m0, X, bytes, a.h, a.N, 0, box, 1);
+  p.X = X;
+  CUtensorMap m1;
   // 128 + 128 columns a tile; 64 + 64 where the expert has no more
   const int half = a.s <= 64 ? 64 : 128;
   MORE_MAP(&m1, a.W_up, bytes, a.h, 2 * (int64_t)a.s, a.M, box, half);
   p.nc = tiles_of(a.s, half);
   const int64_t items = max_tiles(a.S(), a.M) * p.nc;
-  if (half == 64) return launch<MODE, 64>(a, p, items, m0, m1, m0, m0);
-  return launch<MODE, 128>(a, p, items, m0, m1, m0, m0);
+  if (half == 64) return launch<MODE, 64>(a, p, items, m1, m1, m1, m1);
+  return launch<MODE, 128>(a, p, items, m1, m1, m1, m1);
 }
 
 template <int MODE>
@@ -742,14 +807,14 @@ cudaError_t launch_experts_backward(const ExpertsArgs& a) {
   const Buffers b = carve(a.scratch, a.N, a.h, a.s, a.M, a.k, kBackward);
   const int64_t S = a.S(), R = max_rows(S, a.M);
   MORE_TRY(launch_rows(a, b.rows));
-  CUtensorMap mX, mD, m1, m2, m3;
+  CUtensorMap m1, m2, m3;
   Params p = {};
   p.rows = b.rows;
   p.R = R;
   p.s = a.s;
   p.h = a.h;
-  MORE_MAP(&mX, a.X, 2, a.h, a.N, 0, 64, 1);
-  MORE_MAP(&mD, a.out_bar, 2, a.h, a.N, 0, 64, 1);
+  p.X = a.X;
+  p.out_bar = a.out_bar;
   {
     Params q = p;
     q.k1 = q.k2 = a.h;
@@ -760,7 +825,7 @@ cudaError_t launch_experts_backward(const ExpertsArgs& a) {
     q.nc = tiles_of(a.s, 64);
     MORE_MAP(&m1, a.W_up, 2, a.h, 2 * (int64_t)a.s, a.M, 64, 64);
     MORE_MAP(&m3, a.W_down, 2, a.s, a.h, a.M, 64, 64);
-    MORE_TRY((launch<kBack, 64>(a, q, max_tiles(S, a.M) * q.nc, mX, m1, mD, m3)));
+    MORE_TRY((launch<kBack, 64>(a, q, max_tiles(S, a.M) * q.nc, m1, m1, m1, m3)));
   }
   {
     Params q = p;
@@ -780,7 +845,7 @@ cudaError_t launch_experts_backward(const ExpertsArgs& a) {
     q.items = a.M * q.nm * q.nc;
     MORE_MAP(&m1, b.pre, 2, 2 * (int64_t)a.s, R, 0, 64, 64);
     MORE_MAP(&m2, a.W_up_bar, 2, a.h, 2 * (int64_t)a.s, a.M, 64, 32);
-    MORE_TRY((launch<kDwUp, 64>(a, q, q.items, m1, mX, m2, m1)));
+    MORE_TRY((launch<kDwUp, 64>(a, q, q.items, m1, m1, m2, m1)));
   }
   {
     Params q = p;
@@ -790,7 +855,7 @@ cudaError_t launch_experts_backward(const ExpertsArgs& a) {
     q.items = a.M * q.nm * q.nc;
     MORE_MAP(&m1, b.mid, 2, a.s, R, 0, 64, 64);
     MORE_MAP(&m2, a.W_down_bar, 2, a.s, a.h, a.M, 64, 32);
-    MORE_TRY((launch<kDwDown, 64>(a, q, q.items, mD, m1, m2, m1)));
+    MORE_TRY((launch<kDwDown, 64>(a, q, q.items, m1, m1, m2, m1)));
   }
   MORE_TRY(launch_gate_grads(a, b.rows, b.part, gate_parts(a.s), R));
   return launch_combine(a, b.rows, static_cast<const __nv_bfloat16*>(b.Y), a.out);
