@@ -128,27 +128,29 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
   return v;
 }
 
-// One thread per 8 columns of a token; the k rows' loads are issued together.
+// A thread takes 8 columns of a token (and those `across` threads further on); `across`, a power of two, threads a
+// token.  Four rows' loads are in flight a thread, and the small register count keeps every thread slot of the SM busy:
+// that, not the loads a thread, is what reaches the memory's bandwidth here.
 __global__ void __launch_bounds__(256)
     combine_kernel(const __nv_bfloat16* __restrict__ y, const int32_t* __restrict__ slot_row, int64_t N, int h, int k,
-                   __nv_bfloat16* __restrict__ out) {
-  const int groups = h >> 3;
-  const int64_t total = N * groups;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t n = i / groups;
-    const int c = (int)(i - n * groups);
+                   int log_across, __nv_bfloat16* __restrict__ out) {
+  const int groups = h >> 3, across = 1 << log_across;
+  const int64_t n = (int64_t)blockIdx.x * (256 >> log_across) + (threadIdx.x >> log_across);
+  if (n >= N) return;
+  const int32_t* rows = slot_row + n * k;
+  for (int c = threadIdx.x & (across - 1); c < groups; c += across) {
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int j0 = 0; j0 < k; j0 += 8) {
-      uint4 v[8];
+    for (int j0 = 0; j0 < k; j0 += 4) {
+      uint4 v[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int row = j0 + j < k ? slot_row[n * k + j0 + j] : -1;
-        v[j] = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(y + (size_t)row * h) + c) : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < 4; ++j) {
+        const int row = j0 + j < k ? __ldg(rows + j0 + j) : -1;
+        v[j] = row >= 0 ? __ldcs(reinterpret_cast<const uint4*>(y + (size_t)row * h) + c) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) add8(acc, v[j]);
+      for (int j = 0; j < 4; ++j) add8(acc, v[j]);
     }
-    *(reinterpret_cast<uint4*>(out + (size_t)n * h) + c) = pack8(acc);
+    reinterpret_cast<uint4*>(out + (size_t)n * h)[c] = pack8(acc);
   }
 }
 
@@ -172,9 +174,14 @@ __global__ void __launch_bounds__(256)
   for (int j = 0; j < k; ++j) logits_bar[n * k + j] = gate[n * k + j] * (gb[j] - dot);
 }
 
-__device__ __forceinline__ int8_t round8(float v, float top) {
-  // 127 v is exact for a bf16 v, so the division's rounding cannot move a value across a half
-  return (int8_t)__float2int_rn(__fdiv_rn(127.f * v, top));
+// round-half-even(127 v / top) for |v| <= top, with `inv` = 127 / top.  127 v is exact for a bf16 v, so the division
+// would round no value across a half; the product with inv is off by less than 127 * 3 * 2^-24 < 2.3e-5, and only a
+// product that close to a half is divided.
+__device__ __forceinline__ int8_t round8(float v, float top, float inv) {
+  const float y = v * inv;
+  int q = __float2int_rn(y);
+  if (fabsf(fabsf(y - (float)q) - 0.5f) < 4e-5f) q = __float2int_rn(__fdiv_rn(127.f * v, top));
+  return (int8_t)q;
 }
 
 __device__ __forceinline__ float block_max(float v, float* warps) {
@@ -188,72 +195,109 @@ __device__ __forceinline__ float block_max(float v, float* warps) {
 }
 
 constexpr int kQuantThreads = 128;
+constexpr int kHeld = 4;  // 16-byte pieces of a row that a thread keeps between the two passes
 
-// One CTA per row (width a multiple of 16); the second reading of the row comes from L1 or L2.
+__device__ __forceinline__ float top8(uint4 w, float top) {
+  const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __bfloat1622float2(p[i]);
+    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+  }
+  return top;
+}
+
+__device__ __forceinline__ uint2 round8x8(uint4 w, float div, float inv) {
+  const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&w);
+  union {
+    int8_t b[8];
+    uint2 u;
+  } o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __bfloat1622float2(p[i]);
+    o.b[2 * i] = round8(f.x, div, inv);
+    o.b[2 * i + 1] = round8(f.y, div, inv);
+  }
+  return o.u;
+}
+
+// One CTA per row (width a multiple of 16).  The first 4096 values stay in registers between finding the largest and
+// rounding; what is beyond is read again.
 __global__ void __launch_bounds__(kQuantThreads)
     quantize_bf16_kernel(const __nv_bfloat16* __restrict__ v, int width, int8_t* __restrict__ q,
                          float* __restrict__ scale) {
   __shared__ float warps[kQuantThreads / 32];
   const size_t row = blockIdx.x;
   const uint4* src = reinterpret_cast<const uint4*>(v + row * width);
+  const int n = width / 8;
+  uint4 held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int c = threadIdx.x + i * kQuantThreads;
+    held[i] = c < n ? src[c] : make_uint4(0, 0, 0, 0);
+  }
   float top = 0.f;
-  for (int c = threadIdx.x; c < width / 8; c += kQuantThreads) {
-    const uint4 w = src[c];
-    const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&w);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(p[i]);
-      top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-    }
-  }
+  for (int i = 0; i < kHeld; ++i) top = top8(held[i], top);
+  for (int c = threadIdx.x + kHeld * kQuantThreads; c < n; c += kQuantThreads) top = top8(src[c], top);
   top = block_max(top, warps);
-  const float div = top > 0.f ? top : 1.f;
+  const float div = top > 0.f ? top : 1.f, inv = __fdiv_rn(127.f, div);
   uint2* dst = reinterpret_cast<uint2*>(q + row * width);
-  for (int c = threadIdx.x; c < width / 8; c += kQuantThreads) {
-    const uint4 w = src[c];
-    const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&w);
-    union {
-      int8_t b[8];
-      uint2 u;
-    } o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(p[i]);
-      o.b[2 * i] = round8(f.x, div);
-      o.b[2 * i + 1] = round8(f.y, div);
-    }
-    dst[c] = o.u;
+  for (int i = 0; i < kHeld; ++i) {
+    const int c = threadIdx.x + i * kQuantThreads;
+    if (c < n) dst[c] = round8x8(held[i], div, inv);
   }
+  for (int c = threadIdx.x + kHeld * kQuantThreads; c < n; c += kQuantThreads) dst[c] = round8x8(src[c], div, inv);
   if (threadIdx.x == 0) scale[row] = __fdiv_rn(top, 127.f);
 }
 
-// One warp per row of the tiles' slots.
+constexpr int kRowsPerBlock = 32;
+
+// Four rows a warp, one after the other; the first 1024 values of a row stay in registers.
 __global__ void __launch_bounds__(256)
     quantize_rows_kernel(const float* __restrict__ v, int width, Rows r, int8_t* __restrict__ q,
                          float* __restrict__ scale) {
   const int lane = threadIdx.x & 31;
   if ((int)blockIdx.x >= *r.n_tiles) return;
   const int4 t = r.tiles[blockIdx.x];
-  for (int i = threadIdx.x >> 5; i < t.z; i += blockDim.x >> 5) {
+  const int n = width / 4;
+  for (int i = blockIdx.y * kRowsPerBlock + (threadIdx.x >> 5); i < min(t.z, (int)(blockIdx.y + 1) * kRowsPerBlock);
+       i += blockDim.x >> 5) {
     const size_t row = t.y + i;
     const float4* src = reinterpret_cast<const float4*>(v + row * width);
-    float top = 0.f;
-    for (int c = lane; c < width / 4; c += 32) {
-      const float4 f = src[c];
-      top = fmaxf(fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f.z), fabsf(f.w)));
+    float4 held[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = lane + 32 * j;
+      held[j] = c < n ? src[c] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    auto top4 = [](float4 f, float top) {
+      return fmaxf(fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f.z), fabsf(f.w)));
+    };
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = top4(held[j], top);
+    for (int c = lane + 256; c < n; c += 32) top = top4(src[c], top);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float div = top > 0.f ? top : 1.f;
-    for (int c = lane; c < width / 4; c += 32) {
-      const float4 f = src[c];
+    const float div = top > 0.f ? top : 1.f, inv = __fdiv_rn(127.f, div);
+    auto round4 = [&](float4 f) {
       char4 o;
-      o.x = round8(f.x, div);
-      o.y = round8(f.y, div);
-      o.z = round8(f.z, div);
-      o.w = round8(f.w, div);
-      reinterpret_cast<char4*>(q + row * width)[c] = o;
+      o.x = round8(f.x, div, inv);
+      o.y = round8(f.y, div, inv);
+      o.z = round8(f.z, div, inv);
+      o.w = round8(f.w, div, inv);
+      return o;
+    };
+    char4* dst = reinterpret_cast<char4*>(q + row * width);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = lane + 32 * j;
+      if (c < n) dst[c] = round4(held[j]);
     }
+    for (int c = lane + 256; c < n; c += 32) dst[c] = round4(src[c]);
     if (lane == 0) scale[row] = __fdiv_rn(top, 127.f);
   }
 }
@@ -271,9 +315,11 @@ cudaError_t launch_rows(const ExpertsArgs& a, const Rows& r) {
 }
 
 cudaError_t launch_combine(const ExpertsArgs& a, const Rows& r, const __nv_bfloat16* y, void* out) {
-  const int64_t work = a.N * (a.h / 8);
-  const unsigned grid = (unsigned)std::min<int64_t>((work + 255) / 256, 1 << 20);
-  combine_kernel<<<grid, 256, 0, a.stream>>>(y, r.slot_row, a.N, a.h, a.k, static_cast<__nv_bfloat16*>(out));
+  int log_across = 0;
+  while (log_across < 8 && (1 << log_across) < a.h / 8) ++log_across;
+  const int tokens = 256 >> log_across;
+  combine_kernel<<<(unsigned)((a.N + tokens - 1) / tokens), 256, 0, a.stream>>>(
+      y, r.slot_row, a.N, a.h, a.k, log_across, static_cast<__nv_bfloat16*>(out));
   return cudaGetLastError();
 }
 
@@ -292,7 +338,8 @@ cudaError_t launch_quantize_bf16(const __nv_bfloat16* v, int64_t rows, int width
 
 cudaError_t launch_quantize_rows(const ExpertsArgs& a, const Rows& r, const float* v, int width, int8_t* q,
                                  float* scale) {
-  quantize_rows_kernel<<<(unsigned)max_tiles(a.S(), a.M), 256, 0, a.stream>>>(v, width, r, q, scale);
+  const dim3 grid((unsigned)max_tiles(a.S(), a.M), kTileRows / kRowsPerBlock);
+  quantize_rows_kernel<<<grid, 256, 0, a.stream>>>(v, width, r, q, scale);
   return cudaGetLastError();
 }
 

@@ -14,7 +14,7 @@
 // A CTA holds 128 rows of one expert (128 output channels for the weights' gradients) on the TMEM lanes and up
 // to 256 columns:
 //   warp 0       TMA: stages of 128 bytes of K (64 values of 16 bits, 128 of 8), 128B-swizzled;
-//   warps 12-15  asynchronous copies of the rows that are picked by token;
+//   warps 2, 3, 12, 13  asynchronous copies of the rows that are picked by token;
 //   warp 1       tcgen05 MMAs into two accumulators in TMEM, so a tile's epilogue runs under the next one's products;
 //   warps 4-11   epilogue, two warps a lane group.
 // The grid is persistent; tiles come from the row layout that the same call made on the device.
@@ -35,12 +35,13 @@ using namespace sm100;
 
 enum Mode { kUp, kDown, kUp8, kDown8, kBack, kDx, kDwUp, kDwDown };
 
-constexpr int kThreads = 16 * 32;
+constexpr int kThreads = 14 * 32;
 constexpr int kEpiWarps = 8;
 constexpr int kGatherWarps = 4;
 constexpr uint32_t kABytes = kTileRows * 128;  // 16 KB: 128 rows (or 2 boxes of 64 channels x 64 rows) of a stage
 constexpr uint32_t kBox = 64 * 128;            // 8 KB: a box of 64 rows x 128 bytes
 constexpr uint32_t kStageOut = 32 * 128;       // a warp's staging: 32 rows x 64 bf16 columns
+constexpr int kScales = 128;  // column scales that a warp needs of a tile
 constexpr int kMaxStages = 6;
 
 template <int MODE, int HALF>
@@ -54,15 +55,17 @@ struct Shape {
   // columns of one accumulator, and its place in TMEM
   static constexpr int kCols = kIsUp ? 2 * HALF : MODE == kBack ? 3 * HALF : 256;
   static constexpr int kAccStride = kCols <= 128 ? 128 : 256;
-  static constexpr uint32_t kTmemCols = 2 * kAccStride;
+  static constexpr int kAccs = kCols > 256 ? 1 : 2;
+  static constexpr uint32_t kTmemCols = kCols > 256 ? 512 : 2 * kAccStride;
   static constexpr int kBN = kIsUp || MODE == kBack ? HALF : 256;  // output columns of a tile
   static constexpr uint32_t kBBytes = kIsUp || MODE == kBack ? 2 * HALF * 128 : 256 * 128;
   static constexpr uint32_t kStage = kABytes + kBBytes;
-  static constexpr int kStages = kStage > 32 * 1024 ? 4 : 6;
+  static constexpr int kStages = MODE == kDown8 ? 3 : kStage > 32 * 1024 ? 4 : 6;
   static constexpr int kKBlock = kEight ? 128 : 64;
   static constexpr int kKStep = kEight ? 32 : 16;
   static constexpr uint32_t kOffOut = kStages * kStage;
-  static constexpr uint32_t kOffBar = kOffOut + (kStaged ? kEpiWarps * kStageOut : 0);
+  static constexpr uint32_t kOffScale = kOffOut + (kStaged ? kEpiWarps * kStageOut : 0);
+  static constexpr uint32_t kOffBar = kOffScale + (kEight ? kEpiWarps * kScales * 4 : 0);
   static constexpr uint32_t kSmem = kOffBar + (2 * kMaxStages + 4 + 1) * 8 + 16 + 1024;
 };
 
@@ -79,7 +82,7 @@ struct Params {
   const void* out_bar;
   void* out;      // kUp: H; kUp8: H in fp32; kDown, kDx: rows of h; kBack: [da, db]
   __nv_bfloat16* out2;  // kBack: gate * m
-  float* part;          // kBack: the gate's gradient, a partial sum per 32 columns
+  float* part;          // kBack: the gate's gradient, a partial sum per HALF / 2 columns
   const float* row_scale;  // kUp8: by token; kDown8: by row
   const float* col_scale;
   unsigned int* status;
@@ -201,8 +204,9 @@ __device__ void box_loads(const Params& p, const Bars& b, uint8_t* smem, const C
             tma_load_3d(st + kABytes, m1, bar, x, k.c0, k.expert);
             tma_load_3d(st + kABytes + HALF * 128, m1, bar, x, k.c0 + p.s, k.expert);
           } else {
-            mbar_arrive_expect_tx(bar, kBox);
-            tma_load_3d(st + kABytes, m3, bar, k.c0, x - (p.k1 + 63) / 64 * 64, k.expert);
+            mbar_arrive_expect_tx(bar, HALF / 64 * kBox);
+            for (int i = 0; i < HALF / 64; ++i)
+              tma_load_3d(st + kABytes + i * kBox, m3, bar, k.c0 + 64 * i, x - (p.k1 + 63) / 64 * 64, k.expert);
           }
         } else {
           mbar_arrive_expect_tx(bar, S::kStage);
@@ -371,7 +375,7 @@ __device__ void mma_role(const Params& p, const Bars& b, uint8_t* smem, uint32_t
       }
     }
     mma_commit(&b.acc_full[d.i]);
-    d.next(2);
+    d.next(S::kAccs);
   }
 done:
   mma_commit(b.drain);
@@ -384,10 +388,14 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ float sigmoid(float a) { return __fdividef(1.f, 1.f + expf(-a)); }
+// int32 to fp32.  `small`: every |v| < 2^22, where the value drops into a float's mantissa with full-rate
+// instructions; conversions run at an eighth of that rate, and a second product of 64 values a row is one MMA step of
+// work for 256 columns of conversions.
+__device__ __forceinline__ float from_int(uint32_t v, bool small) {
+  return small ? __uint_as_float(v + 0x4b400000u) - 12582912.f : (float)(int)v;
+}
 
-// 32 TMEM columns of this warp's lanes.
-__device__ __forceinline__ void load32(uint32_t taddr, uint32_t* v) { tmem_ld_x32(taddr, v); }
+__device__ __forceinline__ float sigmoid(float a) { return __fdividef(1.f, 1.f + expf(-a)); }
 
 template <int MODE, int HALF>
 __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t tmem, const CUtensorMap* m_out) {
@@ -396,8 +404,10 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
   const int sp = warp & 3, hh = (warp - 4) >> 2;
   const int t = sp * 32 + lane;  // this thread's row of the tile
   const uint32_t lanes = (uint32_t)(sp * 32) << 16;
+  float* scales = reinterpret_cast<float*>(smem + S::kOffScale) + (warp - 4) * kScales;
   uint4* stage = reinterpret_cast<uint4*>(smem + S::kOffOut + (warp - 4) * kStageOut);
   RingPos d;
+  const bool small = p.k1 <= (1 << 22) / (128 * 128);
   const int items = work_items<S::kIsDw>(p);
   for (int w = blockIdx.x; w < items; w += gridDim.x) {
     const Work k = work_at<S::kIsDw>(p, w, S::kBN);
@@ -413,19 +423,38 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
       if constexpr (MODE == kUp8) row_factor = in ? p.row_scale[p.rows.row_token[row]] : 0.f;
       if constexpr (MODE == kBack) slot = in ? p.rows.row_slot[row] : -1;
     }
+    if constexpr (S::kEight) {
+      __syncwarp();
+      constexpr int kOwn = MODE == kUp8 ? HALF / 2 : 64;  // columns of a part: A's and B's, or the two chunks'
+#pragma unroll
+      for (int i = 0; i < 2 * kOwn; i += 32) {
+        const int part = (i + lane) / kOwn, x = (i + lane) % kOwn;
+        const int col = MODE == kUp8 ? k.c0 + hh * kOwn + x : k.c0 + hh * 64 + part * 128 + x;
+        scales[i + lane] = col < p.cols ? p.col_scale[MODE == kUp8 ? (size_t)(2 * k.expert + part) * p.s + col
+                                                                   : (size_t)k.expert * p.cols + col]
+                                        : 0.f;
+      }
+      __syncwarp();
+    }
     if (!empty) {
       if (!bounded_wait(&b.acc_full[d.i], d.phase, b.abort_flag, p.status)) break;
       tc_fence_after();
     }
     const uint32_t acc = tmem + lanes + d.i * S::kAccStride;
+    if (!S::kIsDw && sp * 32 >= k.padded) {  // none of this warp's rows is in the tile
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.acc_empty[d.i]);
+      d.next(S::kAccs);
+      continue;
+    }
 
     if constexpr (S::kIsUp) {
 #pragma unroll
       for (int c = 0; c < HALF / 2; c += 32) {
         const int col = hh * (HALF / 2) + c;
         uint32_t va[32], vb[32];
-        load32(acc + col, va);
-        load32(acc + HALF + col, vb);
+        tmem_ld_x32(acc + col, va);
+        tmem_ld_x32(acc + HALF + col, vb);
         tmem_wait_ld();
         reg_fence<32>(va);
         reg_fence<32>(vb);
@@ -443,9 +472,8 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
           for (int i = 0; i < 8; ++i) {
             float a, u;
             if constexpr (S::kEight) {
-              const float* sc = p.col_scale + (size_t)k.expert * 2 * p.s + g0 + q + i;
-              a = (float)(int)va[q + i] * (row_factor * __ldg(sc));
-              u = (float)(int)vb[q + i] * (row_factor * __ldg(sc + p.s));
+              a = from_int(va[q + i], small) * (row_factor * scales[c + q + i]);
+              u = from_int(vb[q + i], small) * (row_factor * scales[HALF / 2 + c + q + i]);
             } else {
               a = __uint_as_float(va[q + i]);
               u = __uint_as_float(vb[q + i]);
@@ -463,21 +491,25 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
         }
       }
     } else if constexpr (MODE == kBack) {
-      static_assert(MODE != kBack || HALF == 64, "32 columns a warp");
-      uint32_t va[32], vb[32], vg[32];
-      load32(acc + hh * 32, va);
-      load32(acc + HALF + hh * 32, vb);
-      load32(acc + 2 * HALF + hh * 32, vg);
-      tmem_wait_ld();
-      reg_fence<32>(va);
-      reg_fence<32>(vb);
-      reg_fence<32>(vg);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b.acc_empty[d.i]);
-      const int g0 = k.c0 + hh * 32;
       float dot = 0.f;
-      if (t < k.padded) {
+#pragma unroll 1
+      for (int c = 0; c < HALF / 2; c += 32) {
+        const int col = hh * (HALF / 2) + c;
+        uint32_t va[32], vb[32], vg[32];
+        tmem_ld_x32(acc + col, va);
+        tmem_ld_x32(acc + HALF + col, vb);
+        tmem_ld_x32(acc + 2 * HALF + col, vg);
+        tmem_wait_ld();
+        reg_fence<32>(va);
+        reg_fence<32>(vb);
+        reg_fence<32>(vg);
+        if (c + 32 >= HALF / 2) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b.acc_empty[d.i]);
+        }
+        const int g0 = k.c0 + col;
+        if (t >= k.padded) continue;
         __nv_bfloat16* pre = static_cast<__nv_bfloat16*>(p.out) + (size_t)row * 2 * p.s + g0;
         __nv_bfloat16* mid = p.out2 + (size_t)row * p.s + g0;
 #pragma unroll
@@ -502,8 +534,8 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
           *reinterpret_cast<uint4*>(mid + q) =
               make_uint4(pack2(gm[0], gm[1]), pack2(gm[2], gm[3]), pack2(gm[4], gm[5]), pack2(gm[6], gm[7]));
         }
-        p.part[(size_t)(k.c0 / 32 + hh) * p.R + row] = dot;
       }
+      if (t < k.padded) p.part[(size_t)(k.c0 / (HALF / 2) + hh) * p.R + row] = dot;
     } else {
       // 64 columns at a time through the warp's own staging, 16-byte pieces placed by row so that neither side
       // meets bank conflicts (the 128B swizzle): rows go out as whole 128-byte lines
@@ -517,8 +549,8 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
 #pragma unroll
             for (int i = 0; i < 64; ++i) v[i] = 0u;
           } else {
-            load32(acc + c, v);
-            load32(acc + c + 32, v + 32);
+            tmem_ld_x32(acc + c, v);
+            tmem_ld_x32(acc + c + 32, v + 32);
             tmem_wait_ld();
             reg_fence<64>(v);
           }
@@ -537,9 +569,7 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               if constexpr (MODE == kDown8) {
-                const int col = k.c0 + c + q * 8 + i;
-                const float sc = col < p.cols ? __ldg(p.col_scale + (size_t)k.expert * p.cols + col) : 0.f;
-                f[i] = (float)(int)v[q * 8 + i] * (row_factor * sc);
+                f[i] = from_int(v[q * 8 + i], small) * (row_factor * scales[c / 128 * 64 + q * 8 + i]);
               } else {
                 f[i] = __uint_as_float(v[q * 8 + i]) * row_factor;
               }
@@ -573,7 +603,7 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
         }
       }
     }
-    if (!empty) d.next(2);
+    if (!empty) d.next(S::kAccs);
   }
   if constexpr (S::kIsDw) {
     if (lane == 0) bulk_wait_group<0>();
@@ -595,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&b.full[i], 1 + (S::kGathers ? kGatherWarps * 32 : 0));
       mbar_init(&b.empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < S::kAccs; ++i) {
       mbar_init(&b.acc_full[i], 1);
       mbar_init(&b.acc_empty[i], kEpiWarps);
     }
@@ -617,10 +647,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (lane == 0) mma_role<MODE, HALF>(p, b, smem, tmem);
     __syncwarp();
-  } else if (warp >= 12) {
-    if constexpr (S::kGathers) row_copies<MODE, HALF>(p, b, smem, warp - 12);
+  } else if (warp < 4 || warp >= 12) {
+    if constexpr (S::kGathers) row_copies<MODE, HALF>(p, b, smem, warp < 4 ? warp - 2 : warp - 10);
     __syncwarp();
-  } else if (warp >= 4) {
+  } else {
     epilogue<MODE, HALF>(p, b, smem, tmem, &m2);
   }
   tc_fence_before();
@@ -753,7 +783,7 @@ struct Buffers {
 
 enum Kind { kForward = 0, kInt8 = 1, kBackward = 2 };
 
-int gate_parts(int s) { return (s + 63) / 64 * 2; }
+int gate_parts(int s) { return s <= 64 ? 2 : (s + 127) / 128 * 2; }
 
 Buffers carve(void* scratch, int64_t N, int h, int s, int M, int k, int kind) {
   Buffers b = {};
@@ -822,10 +852,13 @@ cudaError_t launch_experts_backward(const ExpertsArgs& a) {
     q.out = b.pre;
     q.out2 = b.mid;
     q.part = b.part;
-    q.nc = tiles_of(a.s, 64);
-    MORE_MAP(&m1, a.W_up, 2, a.h, 2 * (int64_t)a.s, a.M, 64, 64);
+    // 3 x 128 columns leave TMEM one accumulator, 3 x 64 two; the wide tile reads x and y_bar half as often
+    const int half = a.s <= 64 ? 64 : 128;
+    q.nc = tiles_of(a.s, half);
+    MORE_MAP(&m1, a.W_up, 2, a.h, 2 * (int64_t)a.s, a.M, 64, half);
     MORE_MAP(&m3, a.W_down, 2, a.s, a.h, a.M, 64, 64);
-    MORE_TRY((launch<kBack, 64>(a, q, max_tiles(S, a.M) * q.nc, m1, m1, m1, m3)));
+    MORE_TRY((half == 64 ? launch<kBack, 64>(a, q, max_tiles(S, a.M) * q.nc, m1, m1, m1, m3)
+                         : launch<kBack, 128>(a, q, max_tiles(S, a.M) * q.nc, m1, m1, m1, m3)));
   }
   {
     Params q = p;
