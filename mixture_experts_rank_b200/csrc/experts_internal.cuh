@@ -91,6 +91,17 @@ inline Rows carve_rows(Carver& c, int64_t S, int M) {
   return r;
 }
 
+// round-half-even(127 v / top) for |v| <= top, with `inv` = 127 / top.  127 v is exact for a bf16 v, so the division
+// would round no value across a half; the product with inv is off by less than 127 * 3 * 2^-24 < 2.3e-5, and only a
+// product that close to a half is divided.  Adding 1.5 * 2^23 rounds to a whole number in the mantissa's low bits: the
+// conversion instructions run at an eighth of the rate.
+__device__ __forceinline__ int8_t round8(float v, float top, float inv) {
+  const float y = v * inv;
+  float t = y + 12582912.f;
+  if (fabsf(fabsf(y - (t - 12582912.f)) - 0.5f) < 4e-5f) t = __fdiv_rn(127.f * v, top) + 12582912.f;
+  return (int8_t)__float_as_int(t);
+}
+
 // Lays the rows out from offsets, slots and gates (experts_rows.cu).
 cudaError_t launch_rows(const ExpertsArgs& a, const Rows& r);
 // out[n] = sum over j of y[slot_row[n k + j]], fp32 sums in the order of j, rounded once to bf16.

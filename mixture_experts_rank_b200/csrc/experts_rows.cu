@@ -154,48 +154,31 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// One thread per token.
+// Sixteen lanes a token, one a slot (k <= 16).
 __global__ void __launch_bounds__(256)
     gate_grads_kernel(const float* __restrict__ part, int parts, int64_t R, const int32_t* __restrict__ slot_row,
                       const float* __restrict__ gate, int64_t N, int k, float* __restrict__ gate_bar,
                       float* __restrict__ logits_bar) {
-  const int64_t n = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-  if (n >= N) return;
-  float gb[MORE_KMAX], dot = 0.f;
-  for (int j = 0; j < k; ++j) {
-    const int row = slot_row[n * k + j];
-    float s = 0.f;
-    if (row >= 0)
-      for (int p = 0; p < parts; ++p) s += part[p * R + row];
-    gb[j] = s;
-    dot = fmaf(gate[n * k + j], s, dot);
-    gate_bar[n * k + j] = s;
+  const int64_t n = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int j = threadIdx.x & 15;
+  const bool in = n < N && j < k;
+  const int row = in ? slot_row[n * k + j] : -1;
+  const float g = in ? gate[n * k + j] : 0.f;
+  float s = 0.f;
+  if (row >= 0) {
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p) s += part[p * R + row];
   }
-  for (int j = 0; j < k; ++j) logits_bar[n * k + j] = gate[n * k + j] * (gb[j] - dot);
-}
-
-// round-half-even(127 v / top) for |v| <= top, with `inv` = 127 / top.  127 v is exact for a bf16 v, so the division
-// would round no value across a half; the product with inv is off by less than 127 * 3 * 2^-24 < 2.3e-5, and only a
-// product that close to a half is divided.
-__device__ __forceinline__ int8_t round8(float v, float top, float inv) {
-  const float y = v * inv;
-  int q = __float2int_rn(y);
-  if (fabsf(fabsf(y - (float)q) - 0.5f) < 4e-5f) q = __float2int_rn(__fdiv_rn(127.f * v, top));
-  return (int8_t)q;
-}
-
-__device__ __forceinline__ float block_max(float v, float* warps) {
+  float dot = g * s;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float m = warps[0];
-  for (int w = 1; w < (int)blockDim.x >> 5; ++w) m = fmaxf(m, warps[w]);
-  return m;
+  for (int d = 8; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+  if (in) {
+    gate_bar[n * k + j] = s;
+    logits_bar[n * k + j] = g * (s - dot);
+  }
 }
 
-constexpr int kQuantThreads = 128;
-constexpr int kHeld = 4;  // 16-byte pieces of a row that a thread keeps between the two passes
+constexpr int kHeld = 8;  // 16-byte pieces of a row that a lane keeps between the two passes
 
 __device__ __forceinline__ float top8(uint4 w, float top) {
   const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&w);
@@ -222,35 +205,37 @@ __device__ __forceinline__ uint2 round8x8(uint4 w, float div, float inv) {
   return o.u;
 }
 
-// One CTA per row (width a multiple of 16).  The first 4096 values stay in registers between finding the largest and
-// rounding; what is beyond is read again.
-__global__ void __launch_bounds__(kQuantThreads)
-    quantize_bf16_kernel(const __nv_bfloat16* __restrict__ v, int width, int8_t* __restrict__ q,
+// One warp per row (width a multiple of 16): no barrier, and enough rows in flight to cover the latency of one.  The
+// first 2048 values stay in registers between finding the largest and rounding; what is beyond is read again.
+__global__ void __launch_bounds__(128)
+    quantize_bf16_kernel(const __nv_bfloat16* __restrict__ v, int64_t rows, int width, int8_t* __restrict__ q,
                          float* __restrict__ scale) {
-  __shared__ float warps[kQuantThreads / 32];
-  const size_t row = blockIdx.x;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
   const uint4* src = reinterpret_cast<const uint4*>(v + row * width);
   const int n = width / 8;
   uint4 held[kHeld];
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
-    const int c = threadIdx.x + i * kQuantThreads;
+    const int c = lane + i * 32;
     held[i] = c < n ? src[c] : make_uint4(0, 0, 0, 0);
   }
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) top = top8(held[i], top);
-  for (int c = threadIdx.x + kHeld * kQuantThreads; c < n; c += kQuantThreads) top = top8(src[c], top);
-  top = block_max(top, warps);
+  for (int c = lane + kHeld * 32; c < n; c += 32) top = top8(src[c], top);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   const float div = top > 0.f ? top : 1.f, inv = __fdiv_rn(127.f, div);
   uint2* dst = reinterpret_cast<uint2*>(q + row * width);
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
-    const int c = threadIdx.x + i * kQuantThreads;
+    const int c = lane + i * 32;
     if (c < n) dst[c] = round8x8(held[i], div, inv);
   }
-  for (int c = threadIdx.x + kHeld * kQuantThreads; c < n; c += kQuantThreads) dst[c] = round8x8(src[c], div, inv);
-  if (threadIdx.x == 0) scale[row] = __fdiv_rn(top, 127.f);
+  for (int c = lane + kHeld * 32; c < n; c += 32) dst[c] = round8x8(src[c], div, inv);
+  if (lane == 0) scale[row] = __fdiv_rn(top, 127.f);
 }
 
 constexpr int kRowsPerBlock = 32;
@@ -315,8 +300,17 @@ cudaError_t launch_rows(const ExpertsArgs& a, const Rows& r) {
 }
 
 cudaError_t launch_combine(const ExpertsArgs& a, const Rows& r, const __nv_bfloat16* y, void* out) {
-  int log_across = 0;
-  while (log_across < 8 && (1 << log_across) < a.h / 8) ++log_across;
+  // threads a token: up to 256, fewer where that leaves more of them without a column (h = 1096: 137 groups of 8
+  // columns are 5 rounds of 32 threads, 160 places, but 256 places with 128 or 256 threads)
+  const int groups = a.h / 8;
+  int log_across = 0, places = 1 << 30;
+  for (int l = 8; l >= 5; --l) {
+    const int here = (groups + (1 << l) - 1) >> l << l;
+    if (here < places) {
+      places = here;
+      log_across = l;
+    }
+  }
   const int tokens = 256 >> log_across;
   combine_kernel<<<(unsigned)((a.N + tokens - 1) / tokens), 256, 0, a.stream>>>(
       y, r.slot_row, a.N, a.h, a.k, log_across, static_cast<__nv_bfloat16*>(out));
@@ -324,7 +318,7 @@ cudaError_t launch_combine(const ExpertsArgs& a, const Rows& r, const __nv_bfloa
 }
 
 cudaError_t launch_gate_grads(const ExpertsArgs& a, const Rows& r, const float* part, int parts, int64_t R) {
-  gate_grads_kernel<<<(unsigned)((a.N + 255) / 256), 256, 0, a.stream>>>(part, parts, R, r.slot_row, a.gate, a.N, a.k,
+  gate_grads_kernel<<<(unsigned)((a.N + 15) / 16), 256, 0, a.stream>>>(part, parts, R, r.slot_row, a.gate, a.N, a.k,
                                                                           a.gate_bar, a.logits_bar);
   return cudaGetLastError();
 }
@@ -332,7 +326,7 @@ cudaError_t launch_gate_grads(const ExpertsArgs& a, const Rows& r, const float* 
 cudaError_t launch_quantize_bf16(const __nv_bfloat16* v, int64_t rows, int width, int8_t* q, float* scale,
                                  cudaStream_t stream) {
   if (rows == 0) return cudaSuccess;
-  quantize_bf16_kernel<<<(unsigned)rows, kQuantThreads, 0, stream>>>(v, width, q, scale);
+  quantize_bf16_kernel<<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(v, rows, width, q, scale);
   return cudaGetLastError();
 }
 

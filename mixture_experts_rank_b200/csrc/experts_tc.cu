@@ -65,7 +65,8 @@ struct Shape {
   static constexpr int kKStep = kEight ? 32 : 16;
   static constexpr uint32_t kOffOut = kStages * kStage;
   static constexpr uint32_t kOffScale = kOffOut + (kStaged ? kEpiWarps * kStageOut : 0);
-  static constexpr uint32_t kOffBar = kOffScale + (kEight ? kEpiWarps * kScales * 4 : 0);
+  static constexpr uint32_t kOffTop = kOffScale + (kEight ? kEpiWarps * kScales * 4 : 0);
+  static constexpr uint32_t kOffBar = kOffTop + (MODE == kUp8 ? 2 * 256 * 4 : 0);
   static constexpr uint32_t kSmem = kOffBar + (2 * kMaxStages + 4 + 1) * 8 + 16 + 1024;
 };
 
@@ -80,7 +81,8 @@ struct Params {
   int cols;       // output columns
   const void* X;        // the rows picked by token, and kBack's second set
   const void* out_bar;
-  void* out;      // kUp: H; kUp8: H in fp32; kDown, kDx: rows of h; kBack: [da, db]
+  float* out_scale;  // kUp8 with an expert's whole middle in a tile: the rows' scales
+  void* out;      // kUp: H; kUp8: H in fp32, or in 8 bits with out_scale; kDown, kDx: rows of h; kBack: [da, db]
   __nv_bfloat16* out2;  // kBack: gate * m
   float* part;          // kBack: the gate's gradient, a partial sum per HALF / 2 columns
   const float* row_scale;  // kUp8: by token; kDown8: by row
@@ -141,6 +143,31 @@ __device__ __forceinline__ Work work_at(const Params& p, int w, int bn) {
   return k;
 }
 
+// This CTA's tiles in turn.  The next tile's entry is fetched a tile ahead: its latency (two dependent reads with the
+// rows' own) is that of a whole tile of a short product.
+template <bool DW>
+struct Cursor {
+  int w, items, bn;
+  Work cur, nxt;
+  __device__ __forceinline__ Cursor(const Params& p, int bn_) : bn(bn_) {
+    items = work_items<DW>(p);
+    w = blockIdx.x;
+    cur = nxt = Work{};
+    if (w < items) cur = work_at<DW>(p, w, bn);
+    fetch(p);
+  }
+  __device__ __forceinline__ void fetch(const Params& p) {
+    if (w + (int)gridDim.x < items) nxt = work_at<DW>(p, w + gridDim.x, bn);
+  }
+  __device__ __forceinline__ bool done() const { return w >= items; }
+  __device__ __forceinline__ bool more() const { return w + (int)gridDim.x < items; }
+  __device__ __forceinline__ void next(const Params& p) {
+    w += gridDim.x;
+    cur = nxt;
+    fetch(p);
+  }
+};
+
 // ---- loads -----------------------------------------------------------------------------------------------------
 // Warp 0 issues the operands that come as boxes; kGatherWarps warps copy the rows that are picked by token, 16 bytes a
 // lane, four rows of 128 bytes an instruction, placed as the 128B swizzle places them.  (Gathered TMA loads move no more
@@ -181,9 +208,8 @@ __device__ void box_loads(const Params& p, const Bars& b, uint8_t* smem, const C
   using S = Shape<MODE, HALF>;
   const int lane = threadIdx.x & 31;
   Ring r;
-  const int items = work_items<S::kIsDw>(p);
-  for (int w = blockIdx.x; w < items; w += gridDim.x) {
-    const Work k = work_at<S::kIsDw>(p, w, S::kBN);
+  for (Cursor<S::kIsDw> at(p, S::kBN); !at.done(); at.next(p)) {
+    const Work k = at.cur;
     const int len = S::kIsDw ? k.padded : p.k1 + (MODE == kBack ? (p.k1 + 63) / 64 * 64 - p.k1 + p.k2 : 0);
     for (int x = 0; x < len; x += S::kKBlock) {
       if (!wait_empty<S>(r, b, lane, p.status)) return settle<S>(r, b);
@@ -244,16 +270,15 @@ __device__ void row_copies(const Params& p, const Bars& b, uint8_t* smem, int tu
   const size_t pitch = (size_t)p.h * (S::kEight ? 1 : 2);
   const uint32_t st0 = smem_u32(smem);
   Ring c;
-  const int items = work_items<S::kIsDw>(p);
-  for (int w = blockIdx.x; w < items; w += gridDim.x) {
-    const Work k = work_at<S::kIsDw>(p, w, S::kBN);
+  int tok[8] = {};
+  for (Cursor<S::kIsDw> at(p, S::kBN); !at.done(); at.next(p)) {
+    const Work k = at.cur;
     if constexpr (S::kIsDw) {
       // stages of 64 rows; boxes of 64 columns: two of y_bar as A, four of x as B
       constexpr int kBoxes = MODE == kDwUp ? 4 : 2;
       const uint8_t* src = static_cast<const uint8_t*>(MODE == kDwUp ? p.X : p.out_bar);
       const int col = MODE == kDwUp ? k.c0 : k.m0;
       const int32_t* tokens = p.rows.row_token + k.row + sub;
-      int tok[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) tok[i] = 4 * (turn + 4 * i) < k.padded ? tokens[4 * (turn + 4 * i)] : 0;
       for (int r0 = 0; r0 < k.padded; r0 += 64) {
@@ -284,16 +309,23 @@ __device__ void row_copies(const Params& p, const Bars& b, uint8_t* smem, int tu
       }
     } else {
       const uint8_t* row[8];
-      uint32_t at[8];
       const uint8_t* X = static_cast<const uint8_t*>(p.X);
-      size_t tok[8];
+      if (at.w == (int)blockIdx.x) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * (turn + 4 * i) + sub;
+          tok[i] = r < k.padded ? p.rows.row_token[k.row + r] : 0;
+        }
+      }
+      int ahead[8];  // the next tile's tokens
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = 4 * (turn + 4 * i) + sub;
-        tok[i] = r < k.padded ? p.rows.row_token[k.row + r] : 0;
+        ahead[i] = at.more() && r < at.nxt.padded ? p.rows.row_token[at.nxt.row + r] : 0;
         row[i] = X + tok[i] * pitch + piece * 16;
-        at[i] = r * 128 + ((piece ^ (r & 7)) << 4);
       }
+      const int r0 = 4 * turn + sub;  // a lane's rows are 16 apart: the same place in the swizzle
+      const uint32_t dst = r0 * 128 + ((piece ^ (r0 & 7)) << 4);
       const int passes = MODE == kBack ? 2 : 1;
       for (int pass = 0; pass < passes; ++pass) {
         if (pass == 1) {
@@ -307,11 +339,14 @@ __device__ void row_copies(const Params& p, const Bars& b, uint8_t* smem, int tu
           const bool ok = x + piece * 16 < (int)pitch;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (4 * (turn + 4 * i) < k.padded) copy16(st + at[i], row[i] + (ok ? x : 0) - (ok ? 0 : piece * 16), ok);
+            if (4 * (turn + 4 * i) < k.padded)
+              copy16(st + dst + i * 2048, row[i] + (ok ? x : 0) - (ok ? 0 : piece * 16), ok);
           arrive_landed(&b.full[c.pos.i]);
-        c.next<S>();
+          c.next<S>();
         }
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) tok[i] = ahead[i];
     }
   }
   wait_copies();
@@ -323,9 +358,8 @@ __device__ void mma_role(const Params& p, const Bars& b, uint8_t* smem, uint32_t
   using S = Shape<MODE, HALF>;
   RingPos s, d;
   const uint32_t st0 = smem_u32(smem);
-  const int items = work_items<S::kIsDw>(p);
-  for (int w = blockIdx.x; w < items; w += gridDim.x) {
-    const Work k = work_at<S::kIsDw>(p, w, S::kBN);
+  for (Cursor<S::kIsDw> at(p, S::kBN); !at.done(); at.next(p)) {
+    const Work k = at.cur;
     if (S::kIsDw && k.padded == 0) continue;  // the epilogue writes zeros
     if (!bounded_wait(&b.acc_empty[d.i], d.phase ^ 1u, b.abort_flag, p.status)) goto done;
     tc_fence_after();
@@ -397,6 +431,49 @@ __device__ __forceinline__ float from_int(uint32_t v, bool small) {
 
 __device__ __forceinline__ float sigmoid(float a) { return __fdividef(1.f, 1.f + expf(-a)); }
 
+// Scale i of those at shared address a, four to a read; i counts up through a group of them in an unrolled loop.
+__device__ __forceinline__ float scale_at(uint32_t a, int i, float4& four) {
+  if ((i & 3) == 0) {
+    const uint4 v = ld_shared_v4(a + i * 4);
+    four = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+  }
+  return (i & 3) == 0 ? four.x : (i & 3) == 1 ? four.y : (i & 3) == 2 ? four.z : four.w;
+}
+
+// What a thread needs of a tile beside the accumulator: its row's factor and slot, the columns' scales.
+template <int MODE, int HALF>
+struct Info {
+  static constexpr int kOwn = MODE == kUp8 ? HALF / 2 : 64;  // columns of a part: A's and B's, or the two chunks'
+  static constexpr int kScaleRegs = Shape<MODE, HALF>::kEight ? 2 * kOwn / 32 : 0;
+  float factor = 1.f;
+  int slot = -1;
+  float scale[kScaleRegs ? kScaleRegs : 1];
+};
+
+template <int MODE, int HALF>
+__device__ __forceinline__ Info<MODE, HALF> row_info(const Params& p, const Work& k, int t, int lane, int hh) {
+  using S = Shape<MODE, HALF>;
+  using I = Info<MODE, HALF>;
+  I r;
+  if constexpr (!S::kIsDw) {
+    const bool in = t < k.padded;
+    const int row = k.row + t;
+    if constexpr (S::kIsDown || MODE == kBack) r.factor = in ? p.rows.row_gate[row] : 0.f;
+    if constexpr (MODE == kDown8) r.factor *= t < k.n ? p.row_scale[row] : 0.f;
+    if constexpr (MODE == kUp8) r.factor = in ? p.row_scale[p.rows.row_token[row]] : 0.f;
+    if constexpr (MODE == kBack) r.slot = in ? p.rows.row_slot[row] : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < I::kScaleRegs; ++i) {
+    const int part = (32 * i + lane) / I::kOwn, x = (32 * i + lane) % I::kOwn;
+    const int col = MODE == kUp8 ? k.c0 + hh * I::kOwn + x : k.c0 + hh * 64 + part * 128 + x;
+    r.scale[i] = col < p.cols ? p.col_scale[MODE == kUp8 ? (size_t)(2 * k.expert + part) * p.s + col
+                                                         : (size_t)k.expert * p.cols + col]
+                              : 0.f;
+  }
+  return r;
+}
+
 template <int MODE, int HALF>
 __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t tmem, const CUtensorMap* m_out) {
   using S = Shape<MODE, HALF>;
@@ -404,38 +481,27 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
   const int sp = warp & 3, hh = (warp - 4) >> 2;
   const int t = sp * 32 + lane;  // this thread's row of the tile
   const uint32_t lanes = (uint32_t)(sp * 32) << 16;
-  float* scales = reinterpret_cast<float*>(smem + S::kOffScale) + (warp - 4) * kScales;
-  uint4* stage = reinterpret_cast<uint4*>(smem + S::kOffOut + (warp - 4) * kStageOut);
+  const uint32_t scales = smem_u32(smem + S::kOffScale) + (warp - 4) * kScales * 4;
+  const uint32_t stage = smem_u32(smem + S::kOffOut) + (warp - 4) * kStageOut;
   RingPos d;
+  Info<MODE, HALF> info;
+  const uint32_t tops = smem_u32(smem + S::kOffTop);  // two tiles' [2][128] largest magnitudes
+  int parity = 0;
   const bool small = p.k1 <= (1 << 22) / (128 * 128);
-  const int items = work_items<S::kIsDw>(p);
-  for (int w = blockIdx.x; w < items; w += gridDim.x) {
-    const Work k = work_at<S::kIsDw>(p, w, S::kBN);
+  for (Cursor<S::kIsDw> at(p, S::kBN); !at.done(); at.next(p)) {
+    const Work k = at.cur;
     const bool empty = S::kIsDw && k.padded == 0;
     const int row = k.row + t;
-    // what the rows need, read before the wait
-    float row_factor = 1.f;
-    int slot = -1;
-    if constexpr (!S::kIsDw) {
-      const bool in = t < k.padded;
-      if constexpr (MODE == kDown || MODE == kBack || MODE == kDown8) row_factor = in ? p.rows.row_gate[row] : 0.f;
-      if constexpr (MODE == kDown8) row_factor *= t < k.n ? p.row_scale[row] : 0.f;
-      if constexpr (MODE == kUp8) row_factor = in ? p.row_scale[p.rows.row_token[row]] : 0.f;
-      if constexpr (MODE == kBack) slot = in ? p.rows.row_slot[row] : -1;
-    }
+    if (at.w == (int)blockIdx.x) info = row_info<MODE, HALF>(p, k, t, lane, hh);
+    const float row_factor = info.factor;
+    const int slot = info.slot;
     if constexpr (S::kEight) {
       __syncwarp();
-      constexpr int kOwn = MODE == kUp8 ? HALF / 2 : 64;  // columns of a part: A's and B's, or the two chunks'
 #pragma unroll
-      for (int i = 0; i < 2 * kOwn; i += 32) {
-        const int part = (i + lane) / kOwn, x = (i + lane) % kOwn;
-        const int col = MODE == kUp8 ? k.c0 + hh * kOwn + x : k.c0 + hh * 64 + part * 128 + x;
-        scales[i + lane] = col < p.cols ? p.col_scale[MODE == kUp8 ? (size_t)(2 * k.expert + part) * p.s + col
-                                                                   : (size_t)k.expert * p.cols + col]
-                                        : 0.f;
-      }
+      for (int i = 0; i < Info<MODE, HALF>::kScaleRegs; ++i) st_shared_f32(scales + (32 * i + lane) * 4, info.scale[i]);
       __syncwarp();
     }
+    if (at.more()) info = row_info<MODE, HALF>(p, at.nxt, t, lane, hh);  // used a tile from now
     if (!empty) {
       if (!bounded_wait(&b.acc_full[d.i], d.phase, b.abort_flag, p.status)) break;
       tc_fence_after();
@@ -448,7 +514,51 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
       continue;
     }
 
-    if constexpr (S::kIsUp) {
+    if (MODE == kUp8 && HALF == 64 && p.out_scale) {
+      // the expert's whole middle is in this tile, half of a row in each of two threads: round it to 8 bits here
+      uint32_t va[32], vb[32];
+      tmem_ld_x32(acc + hh * 32, va);
+      tmem_ld_x32(acc + HALF + hh * 32, vb);
+      tmem_wait_ld();
+      reg_fence<32>(va);
+      reg_fence<32>(vb);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.acc_empty[d.i]);
+      float top = 0.f;
+      float4 sa, sb;
+      const int width = min(32, p.s - hh * 32);  // of this half: 32, 16 or none
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float a = from_int(va[i], small) * (row_factor * scale_at(scales, i, sa));
+        const float u = from_int(vb[i], small) * (row_factor * scale_at(scales + HALF / 2 * 4, i, sb));
+        const float m = a * sigmoid(a) * u;
+        va[i] = __float_as_uint(m);
+        if (i < width) top = fmaxf(top, fabsf(m));
+      }
+      st_shared_f32(tops + (parity * 256 + hh * 128 + t) * 4, top);
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + sp) : "memory");
+      top = fmaxf(top, ld_shared_f32(tops + (parity * 256 + (hh ^ 1) * 128 + t) * 4));
+      parity ^= 1;
+      if (t < k.n) {
+        const float div = top > 0.f ? top : 1.f, inv = __fdiv_rn(127.f, div);
+#pragma unroll
+        for (int i = 0; i < 32; i += 16) {
+          if (i >= width) break;
+          uint32_t o[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            o[q] = 0;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              o[q] |= (uint32_t)(uint8_t)round8(__uint_as_float(va[i + 4 * q + r]), div, inv) << (8 * r);
+          }
+          *reinterpret_cast<uint4*>(static_cast<int8_t*>(p.out) + (size_t)row * p.s + hh * 32 + i) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        if (hh == 0) p.out_scale[row] = __fdiv_rn(top, 127.f);
+      }
+    } else if constexpr (S::kIsUp) {
 #pragma unroll
       for (int c = 0; c < HALF / 2; c += 32) {
         const int col = hh * (HALF / 2) + c;
@@ -468,12 +578,13 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
         for (int q = 0; q < 32; q += 8) {
           if (g0 + q >= p.s || t >= k.n) continue;
           float m[8];
+          float4 sa, sb;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             float a, u;
             if constexpr (S::kEight) {
-              a = from_int(va[q + i], small) * (row_factor * scales[c + q + i]);
-              u = from_int(vb[q + i], small) * (row_factor * scales[HALF / 2 + c + q + i]);
+              a = from_int(va[q + i], small) * (row_factor * scale_at(scales + (c + q) * 4, i, sa));
+              u = from_int(vb[q + i], small) * (row_factor * scale_at(scales + (HALF / 2 + c + q) * 4, i, sb));
             } else {
               a = __uint_as_float(va[q + i]);
               u = __uint_as_float(vb[q + i]);
@@ -566,33 +677,40 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             float f[8];
+            float4 sc;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               if constexpr (MODE == kDown8) {
-                f[i] = from_int(v[q * 8 + i], small) * (row_factor * scales[c / 128 * 64 + q * 8 + i]);
+                f[i] = from_int(v[q * 8 + i], small) * (row_factor * scale_at(scales + (c / 128 * 64 + q * 8) * 4, i, sc));
               } else {
                 f[i] = __uint_as_float(v[q * 8 + i]) * row_factor;
               }
             }
-            stage[lane * 8 + (q ^ (lane & 7))] =
-                make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+            st_shared_v4(stage + lane * 128 + ((q ^ (lane & 7)) << 4),
+                         make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])));
           }
           if constexpr (S::kIsDw) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0 && k.m0 + sp * 32 < (MODE == kDwUp ? 2 * p.s : p.h)) {
-              tma_store_3d(m_out, stage, k.c0 + c, k.m0 + sp * 32, k.expert);
+              tma_store_3d(m_out, smem + S::kOffOut + (warp - 4) * kStageOut, k.c0 + c, k.m0 + sp * 32, k.expert);
               bulk_commit_group();
             }
           } else {
             __syncwarp();
             const int piece = lane & 7, col = k.c0 + c + piece * 8;
+            uint4 o[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const int rr = i * 4 + (lane >> 3), tr = sp * 32 + rr;
+              const int rr = i * 4 + (lane >> 3);
+              o[i] = ld_shared_v4(stage + rr * 128 + ((piece ^ (rr & 7)) << 4));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int tr = sp * 32 + i * 4 + (lane >> 3);
               if (tr < k.n && col < p.cols)
                 *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (size_t)(k.row + tr) * p.cols + col) =
-                    stage[rr * 8 + (piece ^ (rr & 7))];
+                    o[i];
             }
             __syncwarp();
           }
@@ -726,7 +844,8 @@ int tiles_of(int n, int bn) { return (n + bn - 1) / bn; }
 
 // H = silu(X A^T) * (X B^T); x_bytes: 2 for bf16, 1 for 8 bits
 template <int MODE>
-cudaError_t run_up(const ExpertsArgs& a, const Rows& rows, const void* X, const float* x_scale, void* H) {
+cudaError_t run_up(const ExpertsArgs& a, const Rows& rows, const void* X, const float* x_scale, void* H,
+                   float* h_scale = nullptr) {
   constexpr int bytes = MODE == kUp8 ? 1 : 2, box = 128 / bytes;
   Params p = {};
   p.rows = rows;
@@ -736,6 +855,7 @@ cudaError_t run_up(const ExpertsArgs& a, const Rows& rows, const void* X, const 
   p.cols = a.s;
   p.out = H;
   p.row_scale = x_scale;
+  p.out_scale = h_scale;
   p.col_scale = a.up_scale;
   p.X = X;
   CUtensorMap m1;
@@ -795,7 +915,7 @@ Buffers carve(void* scratch, int64_t N, int h, int s, int M, int k, int kind) {
   } else if (kind == kInt8) {
     b.Xq = c.take<int8_t>(N * h);
     b.x_scale = c.take<float>(N);
-    b.H = c.take<float>(R * s);
+    if (s > 64) b.H = c.take<float>(R * s);
     b.Hq = c.take<int8_t>(R * s);
     b.h_scale = c.take<float>(R);
   } else {
@@ -827,8 +947,13 @@ cudaError_t launch_experts_int8(const ExpertsArgs& a) {
   MORE_TRY(launch_rows(a, b.rows));
   MORE_TRY(launch_quantize_bf16(static_cast<const __nv_bfloat16*>(a.X), a.N, a.h, static_cast<int8_t*>(b.Xq),
                                 b.x_scale, a.stream));
-  MORE_TRY(run_up<kUp8>(a, b.rows, b.Xq, b.x_scale, b.H));
-  MORE_TRY(launch_quantize_rows(a, b.rows, static_cast<const float*>(b.H), a.s, static_cast<int8_t*>(b.Hq), b.h_scale));
+  if (a.s <= 64) {  // one tile holds the middle of an expert's rows: rounded to 8 bits in the product's epilogue
+    MORE_TRY(run_up<kUp8>(a, b.rows, b.Xq, b.x_scale, b.Hq, b.h_scale));
+  } else {
+    MORE_TRY(run_up<kUp8>(a, b.rows, b.Xq, b.x_scale, b.H));
+    MORE_TRY(launch_quantize_rows(a, b.rows, static_cast<const float*>(b.H), a.s, static_cast<int8_t*>(b.Hq),
+                                  b.h_scale));
+  }
   MORE_TRY(run_down<kDown8>(a, b.rows, b.Hq, b.h_scale, b.Y));
   return launch_combine(a, b.rows, static_cast<const __nv_bfloat16*>(b.Y), a.out);
 }
