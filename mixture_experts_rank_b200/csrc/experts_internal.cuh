@@ -3,8 +3,7 @@
 //
 // The slots sorted by expert (more_dispatch) are laid out as rows, each expert's rows starting at a
 // multiple of 16 (kRowPad: the K step of a 16-bit MMA, so that a product over an expert's rows can
-// end on a whole step, and a quad of rows is one gathered TMA load).  A tile is up to 128 rows of one
-// expert.  Padding rows repeat the expert's last token and carry slot -1.
+// end on a whole step).  A tile is up to 128 rows of one expert, 256 for CTA pairs.  Padding rows repeat the expert's last token and carry slot -1.
 #pragma once
 #include "more_internal.cuh"
 
@@ -19,7 +18,7 @@ struct Rows {
   int32_t* row_token;  // [R] token of a row (any valid token where row_slot < 0)
   float* row_gate;     // [R] gate of a row's slot (0 where row_slot < 0)
   int32_t* slot_row;   // [S] row of a slot, -1 where no expert lists it
-  int4* tiles;         // [T] {expert, first row, rows that are slots, rows rounded up to kRowPad}
+  int4* tiles;         // [T] {expert, first row, rows that are slots (at most the call's tile_rows), those padded}
   int32_t* row_start;  // [M + 1] first row of each expert
   int32_t* n_tiles;    // [1]
 };
@@ -54,7 +53,7 @@ inline int64_t max_rows(int64_t S, int M) {
   const int64_t used = S < M ? S : M;
   return (S + used * (kRowPad - 1) + kTileRows - 1) / kTileRows * kTileRows;
 }
-inline int64_t max_tiles(int64_t S, int M) { return S / kTileRows + (S < M ? S : M); }
+inline int64_t max_tiles(int64_t S, int M, int tile_rows = kTileRows) { return S / tile_rows + (S < M ? S : M); }
 
 // Rows, tiles and work items of every kernel count in 32 bits.
 inline bool experts_supported(int64_t N, int h, int s, int M, int k) {
@@ -103,7 +102,9 @@ __device__ __forceinline__ int8_t round8(float v, float top, float inv) {
 }
 
 // Lays the rows out from offsets, slots and gates (experts_rows.cu).
-cudaError_t launch_rows(const ExpertsArgs& a, const Rows& r);
+cudaError_t launch_rows(const ExpertsArgs& a, const Rows& r, int tile_rows);
+// Rows of `pitch` bytes (a multiple of 16) picked by token into the padded layout.
+cudaError_t launch_pick(const ExpertsArgs& a, const Rows& r, const void* src, int pitch, void* dst);
 // out[n] = sum over j of y[slot_row[n k + j]], fp32 sums in the order of j, rounded once to bf16.
 cudaError_t launch_combine(const ExpertsArgs& a, const Rows& r, const __nv_bfloat16* y, void* out);
 // gate_bar[slot] = the sum of `parts` partial sums [parts][R] in order, and the logits' gradient
@@ -114,7 +115,7 @@ cudaError_t launch_quantize_bf16(const __nv_bfloat16* v, int64_t rows, int width
                                  cudaStream_t stream);
 // The same for the rows that a call uses of an fp32 [R][width] buffer (every tile's slots).
 cudaError_t launch_quantize_rows(const ExpertsArgs& a, const Rows& r, const float* v, int width, int8_t* q,
-                                 float* scale);
+                                 float* scale, int tile_rows);
 
 // The selected experts of a few tokens (moe_layer.cu).  Xq and the scales: 8-bit weights.
 struct FewArgs {

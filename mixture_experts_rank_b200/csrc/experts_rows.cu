@@ -45,7 +45,8 @@ __device__ void scan_pairs(int& rows, int& tiles, int* warp_rows, int* warp_tile
 // over the threads writes the experts' first rows and tiles.  Offsets that fall, or lie outside
 // [0, S], set MORE_DEVERR_BAD_INPUT and leave no expert with rows.
 __global__ void __launch_bounds__(kScanThreads)
-    rows_scan_kernel(const int32_t* __restrict__ offsets, int64_t S, int M, Rows out, unsigned int* status) {
+    rows_scan_kernel(const int32_t* __restrict__ offsets, int64_t S, int M, int tile_rows, Rows out,
+                     unsigned int* status) {
   __shared__ int warp_rows[kScanThreads / 32], warp_tiles[kScanThreads / 32];
   __shared__ int bad;
   const int run = (M + kScanThreads - 1) / kScanThreads;
@@ -60,7 +61,7 @@ __global__ void __launch_bounds__(kScanThreads)
     if (next < at || next > S) broken = 1;
     const int n = max(0, next - at);
     rows += (n + kRowPad - 1) / kRowPad * kRowPad;
-    tiles += (n + kTileRows - 1) / kTileRows;
+    tiles += (n + tile_rows - 1) / tile_rows;
     at = next;
   }
   if (broken) atomicOr(&bad, 1);
@@ -75,8 +76,8 @@ __global__ void __launch_bounds__(kScanThreads)
     out.row_start[e] = rows;
     if (!none) {
       const int n = next - at;
-      for (int r = 0; r < n; r += kTileRows) {
-        const int here = min(n - r, kTileRows);
+      for (int r = 0; r < n; r += tile_rows) {
+        const int here = min(n - r, tile_rows);
         out.tiles[tiles++] = make_int4(e, rows + r, here, (here + kRowPad - 1) / kRowPad * kRowPad);
       }
       rows += (n + kRowPad - 1) / kRowPad * kRowPad;
@@ -90,8 +91,8 @@ __global__ void __launch_bounds__(kScanThreads)
   }
 }
 
-// One CTA of 128 threads per tile: the rows' slots, tokens and gates, and each slot's row.
-__global__ void __launch_bounds__(kTileRows)
+// One CTA per tile, a thread per row: the rows' slots, tokens and gates, and each slot's row.
+__global__ void __launch_bounds__(2 * kTileRows)
     rows_fill_kernel(const int32_t* __restrict__ offsets, const int32_t* __restrict__ slots,
                      const float* __restrict__ gate, int64_t S, int k, Rows out, unsigned int* status) {
   if ((int)blockIdx.x >= *out.n_tiles) return;
@@ -151,6 +152,26 @@ __global__ void __launch_bounds__(256)
       for (int j = 0; j < 4; ++j) add8(acc, v[j]);
     }
     reinterpret_cast<uint4*>(out + (size_t)n * h)[c] = pack8(acc);
+  }
+}
+
+// One warp per row of the padded layout, eight pieces of 16 bytes in flight a lane.
+__global__ void __launch_bounds__(256)
+    pick_kernel(const uint4* __restrict__ src, const int32_t* __restrict__ row_token, const int32_t* __restrict__ rows,
+                int pieces, uint4* __restrict__ dst) {
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= *rows) return;
+  const uint4* from = src + (size_t)row_token[row] * pieces;
+  uint4* to = dst + (size_t)row * pieces;
+  for (int c = lane; c < pieces; c += 256) {
+    uint4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + 32 * i < pieces) v[i] = __ldg(from + c + 32 * i);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + 32 * i < pieces) to[c + 32 * i] = v[i];
   }
 }
 
@@ -289,13 +310,19 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
-cudaError_t launch_rows(const ExpertsArgs& a, const Rows& r) {
+cudaError_t launch_rows(const ExpertsArgs& a, const Rows& r, int tile_rows) {
   const int64_t S = a.S();
   cudaError_t e = cudaMemsetAsync(r.slot_row, 0xff, sizeof(int32_t) * (size_t)S, a.stream);
   if (e != cudaSuccess) return e;
-  rows_scan_kernel<<<1, kScanThreads, 0, a.stream>>>(a.offsets, S, a.M, r, a.status);
-  rows_fill_kernel<<<(unsigned)max_tiles(S, a.M), kTileRows, 0, a.stream>>>(a.offsets, a.slots, a.gate, S, a.k, r,
-                                                                             a.status);
+  rows_scan_kernel<<<1, kScanThreads, 0, a.stream>>>(a.offsets, S, a.M, tile_rows, r, a.status);
+  rows_fill_kernel<<<(unsigned)max_tiles(S, a.M, tile_rows), tile_rows, 0, a.stream>>>(a.offsets, a.slots, a.gate, S,
+                                                                                        a.k, r, a.status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pick(const ExpertsArgs& a, const Rows& r, const void* src, int pitch, void* dst) {
+  pick_kernel<<<(unsigned)(max_rows(a.S(), a.M) / 8), 256, 0, a.stream>>>(
+      static_cast<const uint4*>(src), r.row_token, r.row_start + a.M, pitch / 16, static_cast<uint4*>(dst));
   return cudaGetLastError();
 }
 
@@ -331,8 +358,8 @@ cudaError_t launch_quantize_bf16(const __nv_bfloat16* v, int64_t rows, int width
 }
 
 cudaError_t launch_quantize_rows(const ExpertsArgs& a, const Rows& r, const float* v, int width, int8_t* q,
-                                 float* scale) {
-  const dim3 grid((unsigned)max_tiles(a.S(), a.M), kTileRows / kRowsPerBlock);
+                                 float* scale, int tile_rows) {
+  const dim3 grid((unsigned)max_tiles(a.S(), a.M, tile_rows), tile_rows / kRowsPerBlock);
   quantize_rows_kernel<<<grid, 256, 0, a.stream>>>(v, width, r, q, scale);
   return cudaGetLastError();
 }

@@ -35,7 +35,6 @@ using namespace sm100;
 
 enum Mode { kUp, kDown, kUp8, kDown8, kBack, kDx, kDwUp, kDwDown };
 
-constexpr int kThreads = 14 * 32;
 constexpr int kEpiWarps = 8;
 constexpr int kGatherWarps = 4;
 constexpr uint32_t kABytes = kTileRows * 128;  // 16 KB: 128 rows (or 2 boxes of 64 channels x 64 rows) of a stage
@@ -44,13 +43,15 @@ constexpr uint32_t kStageOut = 32 * 128;       // a warp's staging: 32 rows x 64
 constexpr int kScales = 128;  // column scales that a warp needs of a tile
 constexpr int kMaxStages = 6;
 
-template <int MODE, int HALF>
+template <int MODE, int HALF, bool PAIR>
 struct Shape {
   static constexpr bool kEight = MODE == kUp8 || MODE == kDown8;
   static constexpr bool kIsUp = MODE == kUp || MODE == kUp8;
   static constexpr bool kIsDown = MODE == kDown || MODE == kDown8;
   static constexpr bool kIsDw = MODE == kDwUp || MODE == kDwDown;
-  static constexpr bool kGathers = kIsUp || kIsDw || MODE == kBack;  // one operand is picked by token
+  static constexpr bool kGathers = !PAIR && (kIsUp || kIsDw || MODE == kBack);  // one operand is picked by token
+  static constexpr int kThreads = PAIR ? 12 * 32 : 14 * 32;
+  static constexpr int kRows = PAIR ? 2 * kTileRows : kTileRows;  // rows (or channels) of a tile
   static constexpr bool kStaged = kIsDown || MODE == kDx || kIsDw;  // epilogue goes through shared memory
   // columns of one accumulator, and its place in TMEM
   static constexpr int kCols = kIsUp ? 2 * HALF : MODE == kBack ? 3 * HALF : 256;
@@ -58,9 +59,9 @@ struct Shape {
   static constexpr int kAccs = kCols > 256 ? 1 : 2;
   static constexpr uint32_t kTmemCols = kCols > 256 ? 512 : 2 * kAccStride;
   static constexpr int kBN = kIsUp || MODE == kBack ? HALF : 256;  // output columns of a tile
-  static constexpr uint32_t kBBytes = kIsUp || MODE == kBack ? 2 * HALF * 128 : 256 * 128;
+  static constexpr uint32_t kBBytes = PAIR ? 128 * 128 : kIsUp || MODE == kBack ? 2 * HALF * 128 : 256 * 128;
   static constexpr uint32_t kStage = kABytes + kBBytes;
-  static constexpr int kStages = MODE == kDown8 ? 3 : kStage > 32 * 1024 ? 4 : 6;
+  static constexpr int kStages = MODE == kDown8 ? (PAIR ? 5 : 3) : kStage > 32 * 1024 ? 4 : 6;
   static constexpr int kKBlock = kEight ? 128 : 64;
   static constexpr int kKStep = kEight ? 32 : 16;
   static constexpr uint32_t kOffOut = kStages * kStage;
@@ -121,14 +122,14 @@ __device__ __forceinline__ int work_items(const Params& p) {
 }
 
 template <bool DW>
-__device__ __forceinline__ Work work_at(const Params& p, int w, int bn) {
+__device__ __forceinline__ Work work_at(const Params& p, int w, int bn, int rows) {
   Work k;
   if (DW) {
     const int e = w / (p.nm * p.nc), rest = w - e * (p.nm * p.nc);
     k.expert = e;
     k.row = p.rows.row_start[e];
     k.n = k.padded = p.rows.row_start[e + 1] - k.row;
-    k.m0 = rest / p.nc * kTileRows;
+    k.m0 = rest / p.nc * rows;
     k.c0 = rest % p.nc * bn;
   } else {
     const int t = w / p.nc;
@@ -145,24 +146,26 @@ __device__ __forceinline__ Work work_at(const Params& p, int w, int bn) {
 
 // This CTA's tiles in turn.  The next tile's entry is fetched a tile ahead: its latency (two dependent reads with the
 // rows' own) is that of a whole tile of a short product.
-template <bool DW>
+template <class S, bool PAIR>
 struct Cursor {
-  int w, items, bn;
+  int w, items;
   Work cur, nxt;
-  __device__ __forceinline__ Cursor(const Params& p, int bn_) : bn(bn_) {
-    items = work_items<DW>(p);
-    w = blockIdx.x;
+  static __device__ __forceinline__ int first() { return PAIR ? blockIdx.x >> 1 : blockIdx.x; }
+  static __device__ __forceinline__ int stride() { return PAIR ? gridDim.x >> 1 : gridDim.x; }
+  __device__ __forceinline__ Cursor(const Params& p) {
+    items = work_items<S::kIsDw>(p);
+    w = first();
     cur = nxt = Work{};
-    if (w < items) cur = work_at<DW>(p, w, bn);
+    if (w < items) cur = work_at<S::kIsDw>(p, w, S::kBN, S::kRows);
     fetch(p);
   }
   __device__ __forceinline__ void fetch(const Params& p) {
-    if (w + (int)gridDim.x < items) nxt = work_at<DW>(p, w + gridDim.x, bn);
+    if (w + stride() < items) nxt = work_at<S::kIsDw>(p, w + stride(), S::kBN, S::kRows);
   }
   __device__ __forceinline__ bool done() const { return w >= items; }
-  __device__ __forceinline__ bool more() const { return w + (int)gridDim.x < items; }
+  __device__ __forceinline__ bool more() const { return w + stride() < items; }
   __device__ __forceinline__ void next(const Params& p) {
-    w += gridDim.x;
+    w += stride();
     cur = nxt;
     fetch(p);
   }
@@ -191,32 +194,71 @@ __device__ __forceinline__ bool wait_empty(const Ring& r, const Bars& b, int lan
 }
 
 // Box loads still in flight when the CTA gives up must land before its shared memory is another's.
-template <class S>
+template <class S, bool PAIR>
 __device__ __noinline__ void settle(const Ring& r, const Bars& b) {
-  for (int i = 0; i < S::kStages; ++i) {
-    const uint32_t fills = (r.issued + S::kStages - 1 - i) / S::kStages;
-    if (fills == 0) continue;
+  if constexpr (PAIR) {  // the loads complete on CTA 0's barriers: a millisecond is hundreds of times what they take
     const uint64_t t0 = global_timer_ns();
-    while (!mbar_test_wait(&b.full[i], (fills - 1) & 1u) && global_timer_ns() - t0 < 1000000000ull) {
+    while (global_timer_ns() - t0 < 1000000ull) {
+    }
+  } else {
+    for (int i = 0; i < S::kStages; ++i) {
+      const uint32_t fills = (r.issued + S::kStages - 1 - i) / S::kStages;
+      if (fills == 0) continue;
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_test_wait(&b.full[i], (fills - 1) & 1u) && global_timer_ns() - t0 < 1000000000ull) {
+      }
     }
   }
 }
 
+// This CTA's part of a pair's stage: its 128 rows (or channels) of A, its half of B's columns.
 template <int MODE, int HALF>
+__device__ __forceinline__ void pair_stage(const Params& p, uint64_t* bar, uint8_t* st, const Work& k, int x, int rank,
+                                           const CUtensorMap* m0, const CUtensorMap* m1, const CUtensorMap* m2,
+                                           const CUtensorMap* m3) {
+  using S = Shape<MODE, HALF, true>;
+  uint8_t* bm = st + kABytes;
+  const int row = k.row + rank * kTileRows;
+  const int round1 = (p.k1 + 63) / 64 * 64;
+  if (rank == 0) mbar_arrive_expect_tx(bar, MODE == kBack && x >= round1 ? 2 * (kABytes + kBox) : 2 * S::kStage);
+  if constexpr (S::kIsDw) {
+    for (int i = 0; i < 2; ++i) {
+      tma_load_2d_pair(st + i * kBox, m0, bar, k.m0 + rank * 128 + 64 * i, k.row + x);
+      tma_load_2d_pair(bm + i * kBox, m1, bar, k.c0 + rank * 128 + 64 * i, k.row + x);
+    }
+  } else if constexpr (MODE == kDx) {
+    tma_load_2d_pair(st, m0, bar, x, row);
+    for (int i = 0; i < 2; ++i)
+      tma_load_3d_pair(bm + i * kBox, m1, bar, k.c0 + rank * 128 + 64 * i, x, k.expert);
+  } else if constexpr (S::kIsDown) {
+    tma_load_2d_pair(st, m0, bar, x, row);
+    tma_load_3d_pair(bm, m1, bar, x, k.c0 + rank * 128, k.expert);
+  } else if (MODE != kBack || x < round1) {
+    tma_load_2d_pair(st, m0, bar, x, row);
+    tma_load_3d_pair(bm, m1, bar, x, k.c0 + rank * p.s, k.expert);  // A_e's rows in CTA 0, B_e's in CTA 1
+  } else {
+    tma_load_2d_pair(st, m2, bar, x - round1, row);
+    tma_load_3d_pair(bm, m3, bar, k.c0 + rank * 64, x - round1, k.expert);
+  }
+}
+
+template <int MODE, int HALF, bool PAIR>
 __device__ void box_loads(const Params& p, const Bars& b, uint8_t* smem, const CUtensorMap* m0, const CUtensorMap* m1,
-                          const CUtensorMap* m3) {
-  using S = Shape<MODE, HALF>;
+                          const CUtensorMap* m2, const CUtensorMap* m3, int rank) {
+  using S = Shape<MODE, HALF, PAIR>;
   const int lane = threadIdx.x & 31;
   Ring r;
-  for (Cursor<S::kIsDw> at(p, S::kBN); !at.done(); at.next(p)) {
+  for (Cursor<S, PAIR> at(p); !at.done(); at.next(p)) {
     const Work k = at.cur;
     const int len = S::kIsDw ? k.padded : p.k1 + (MODE == kBack ? (p.k1 + 63) / 64 * 64 - p.k1 + p.k2 : 0);
     for (int x = 0; x < len; x += S::kKBlock) {
-      if (!wait_empty<S>(r, b, lane, p.status)) return settle<S>(r, b);
+      if (!wait_empty<S>(r, b, lane, p.status)) return settle<S, PAIR>(r, b);
       if (lane == 0) {
         uint64_t* bar = &b.full[r.pos.i];
         uint8_t* st = smem + r.pos.i * S::kStage;
-        if constexpr (MODE == kDwUp) {
+        if constexpr (PAIR) {
+          pair_stage<MODE, HALF>(p, bar, st, k, x, rank, m0, m1, m2, m3);
+        } else if constexpr (MODE == kDwUp) {
           mbar_arrive_expect_tx(bar, 2 * kBox);
           tma_load_2d(st, m0, bar, k.m0, k.row + x);
           tma_load_2d(st + kBox, m0, bar, k.m0 + 64, k.row + x);
@@ -263,15 +305,15 @@ __device__ __forceinline__ void arrive_landed(uint64_t* bar) {
 
 __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-template <int MODE, int HALF>
+template <int MODE, int HALF, bool PAIR>
 __device__ void row_copies(const Params& p, const Bars& b, uint8_t* smem, int turn) {
-  using S = Shape<MODE, HALF>;
+  using S = Shape<MODE, HALF, PAIR>;
   const int lane = threadIdx.x & 31, sub = lane >> 3, piece = lane & 7;
   const size_t pitch = (size_t)p.h * (S::kEight ? 1 : 2);
   const uint32_t st0 = smem_u32(smem);
   Ring c;
   int tok[8] = {};
-  for (Cursor<S::kIsDw> at(p, S::kBN); !at.done(); at.next(p)) {
+  for (Cursor<S, PAIR> at(p); !at.done(); at.next(p)) {
     const Work k = at.cur;
     if constexpr (S::kIsDw) {
       // stages of 64 rows; boxes of 64 columns: two of y_bar as A, four of x as B
@@ -310,7 +352,7 @@ __device__ void row_copies(const Params& p, const Bars& b, uint8_t* smem, int tu
     } else {
       const uint8_t* row[8];
       const uint8_t* X = static_cast<const uint8_t*>(p.X);
-      if (at.w == (int)blockIdx.x) {
+      if (at.w == at.first()) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int r = 4 * (turn + 4 * i) + sub;
@@ -353,12 +395,47 @@ __device__ void row_copies(const Params& p, const Bars& b, uint8_t* smem, int tu
 }
 
 // ---- MMA issuer: one thread --------------------------------------------------------------------------------------
-template <int MODE, int HALF>
+// The products of one stage, `steps` MMAs of K = 16 (or 32 bytes).  A step's operands lie 32 bytes on (K-major) or two
+// groups of eight rows on (MN-major), so its descriptors are the stage's plus a constant: one thread issues everything,
+// and it should not build each descriptor afresh.
+template <bool EIGHT, bool A_MN, bool B_MN, int MAX, bool PAIR>
+__device__ __forceinline__ void stage_products(uint32_t acc, uint64_t a, uint64_t b, uint32_t idesc, int steps,
+                                               bool first) {
+  constexpr uint64_t kA = A_MN ? 2048 >> 4 : 32 >> 4, kB = B_MN ? 2048 >> 4 : 32 >> 4;
+#pragma unroll
+  for (int i = 0; i < MAX; ++i) {
+    if (i > 0 && i >= steps) break;
+    const uint32_t add = i > 0 || !first;
+    if constexpr (EIGHT && PAIR)
+      mma_i8_pair(acc, a + i * kA, b + i * kB, idesc, add);
+    else if constexpr (EIGHT)
+      mma_i8(acc, a + i * kA, b + i * kB, idesc, add);
+    else if constexpr (PAIR)
+      mma_bf16_pair(acc, a + i * kA, b + i * kB, idesc, add);
+    else
+      mma_bf16(acc, a + i * kA, b + i * kB, idesc, add);
+  }
+}
+
+// The MMAs so far are done: tell this CTA's barrier, or both CTAs' of a pair.
+template <bool PAIR>
+__device__ __forceinline__ void done_with(uint64_t* bar) {
+  if constexpr (PAIR)
+    mma_commit_pair(bar, 3);
+  else
+    mma_commit(bar);
+}
+
+template <int MODE, int HALF, bool PAIR>
 __device__ void mma_role(const Params& p, const Bars& b, uint8_t* smem, uint32_t tmem) {
-  using S = Shape<MODE, HALF>;
+  using S = Shape<MODE, HALF, PAIR>;
+  constexpr int kMax = S::kKBlock / S::kKStep;
+  constexpr bool kAMn = S::kIsDw, kBMn = S::kIsDw || MODE == kDx;
   RingPos s, d;
   const uint32_t st0 = smem_u32(smem);
-  for (Cursor<S::kIsDw> at(p, S::kBN); !at.done(); at.next(p)) {
+  const uint64_t a0 = smem_desc(st0, kAMn ? kBox : 16, 1024, kSwizzle128B);
+  const uint64_t b0 = smem_desc(st0 + kABytes, kBMn ? kBox : 16, 1024, kSwizzle128B);
+  for (Cursor<S, PAIR> at(p); !at.done(); at.next(p)) {
     const Work k = at.cur;
     if (S::kIsDw && k.padded == 0) continue;  // the epilogue writes zeros
     if (!bounded_wait(&b.acc_empty[d.i], d.phase ^ 1u, b.abort_flag, p.status)) goto done;
@@ -367,52 +444,40 @@ __device__ void mma_role(const Params& p, const Bars& b, uint8_t* smem, uint32_t
       const uint32_t acc = tmem + d.i * S::kAccStride;
       const int len1 = S::kIsDw ? k.padded : p.k1;
       // columns of this tile's product: all, or up to the last of the weights' gradient, whole MMA steps
-      const int n = MODE == kDwDown ? min(256, (p.cols - k.c0 + 15) & ~15) : S::kIsUp || MODE == kBack ? 2 * HALF : 256;
+      const int n = MODE == kDwDown && !PAIR ? min(256, (p.cols - k.c0 + 15) & ~15) : S::kIsUp || MODE == kBack ? 2 * HALF : 256;
+      const uint32_t idesc = S::kEight ? idesc_s8_s32(S::kRows, n) : idesc_bf16_f32(S::kRows, n, kAMn, kBMn);
       for (int x = 0; x < len1; x += S::kKBlock) {
         if (!bounded_wait(&b.full[s.i], s.phase, b.abort_flag, p.status)) goto done;
         if constexpr (S::kGathers) fence_proxy_async_smem();
         tc_fence_after();
-        const uint32_t a = st0 + s.i * S::kStage, bm = a + kABytes;
-        const int steps = (min(S::kKBlock, len1 - x) + S::kKStep - 1) / S::kKStep;
-        for (int i = 0; i < steps; ++i) {
-          const uint32_t more_ = (x | i) != 0;
-          if constexpr (S::kEight) {
-            mma_i8(acc, smem_desc(a + i * 32, 16, 1024, kSwizzle128B), smem_desc(bm + i * 32, 16, 1024, kSwizzle128B),
-                   idesc_s8_s32(128, n), more_);
-          } else if constexpr (S::kIsDw) {
-            mma_bf16(acc, smem_desc(a + i * 2048, kBox, 1024, kSwizzle128B),
-                     smem_desc(bm + i * 2048, kBox, 1024, kSwizzle128B), idesc_bf16_f32(128, n, 1, 1), more_);
-          } else if constexpr (MODE == kDx) {
-            mma_bf16(acc, smem_desc(a + i * 32, 16, 1024, kSwizzle128B),
-                     smem_desc(bm + i * 2048, kBox, 1024, kSwizzle128B), idesc_bf16_f32(128, n, 0, 1), more_);
-          } else {
-            mma_bf16(acc, smem_desc(a + i * 32, 16, 1024, kSwizzle128B), smem_desc(bm + i * 32, 16, 1024, kSwizzle128B),
-                     idesc_bf16_f32(128, n, 0, 0), more_);
-          }
-        }
-        mma_commit(&b.empty[s.i]);
+        const uint64_t off = (uint32_t)s.i * (S::kStage >> 4);
+        stage_products<S::kEight, kAMn, kBMn, kMax, PAIR>(acc, a0 + off, b0 + off, idesc,
+                                                    (len1 - x + S::kKStep - 1) / S::kKStep, x == 0);
+        done_with<PAIR>(&b.empty[s.i]);
         s.next(S::kStages);
       }
       if constexpr (MODE == kBack) {
+        const uint64_t b1 = smem_desc(st0 + kABytes, kBox, 1024, kSwizzle128B);
         for (int x = 0; x < p.k2; x += S::kKBlock) {
           if (!bounded_wait(&b.full[s.i], s.phase, b.abort_flag, p.status)) goto done;
-          fence_proxy_async_smem();
+          if constexpr (S::kGathers) fence_proxy_async_smem();
           tc_fence_after();
-          const uint32_t a = st0 + s.i * S::kStage, bm = a + kABytes;
-          const int steps = (min(S::kKBlock, p.k2 - x) + S::kKStep - 1) / S::kKStep;
-          for (int i = 0; i < steps; ++i)
-            mma_bf16(acc + 2 * HALF, smem_desc(a + i * 32, 16, 1024, kSwizzle128B),
-                     smem_desc(bm + i * 2048, kBox, 1024, kSwizzle128B), idesc_bf16_f32(128, HALF, 0, 1), (x | i) != 0);
-          mma_commit(&b.empty[s.i]);
+          const uint64_t off = (uint32_t)s.i * (S::kStage >> 4);
+          stage_products<false, false, true, kMax, PAIR>(acc + 2 * HALF, a0 + off, b1 + off, idesc_bf16_f32(S::kRows, HALF, 0, 1),
+                                                   (p.k2 - x + S::kKStep - 1) / S::kKStep, x == 0);
+          done_with<PAIR>(&b.empty[s.i]);
           s.next(S::kStages);
         }
       }
     }
-    mma_commit(&b.acc_full[d.i]);
+    done_with<PAIR>(&b.acc_full[d.i]);
     d.next(S::kAccs);
   }
 done:
-  mma_commit(b.drain);
+  if constexpr (PAIR)
+    mma_commit_pair(b.drain, 1);
+  else
+    mma_commit(b.drain);
   bounded_wait(b.drain, 0, b.abort_flag, p.status);
 }
 
@@ -441,19 +506,19 @@ __device__ __forceinline__ float scale_at(uint32_t a, int i, float4& four) {
 }
 
 // What a thread needs of a tile beside the accumulator: its row's factor and slot, the columns' scales.
-template <int MODE, int HALF>
+template <int MODE, int HALF, bool PAIR>
 struct Info {
   static constexpr int kOwn = MODE == kUp8 ? HALF / 2 : 64;  // columns of a part: A's and B's, or the two chunks'
-  static constexpr int kScaleRegs = Shape<MODE, HALF>::kEight ? 2 * kOwn / 32 : 0;
+  static constexpr int kScaleRegs = Shape<MODE, HALF, PAIR>::kEight ? 2 * kOwn / 32 : 0;
   float factor = 1.f;
   int slot = -1;
   float scale[kScaleRegs ? kScaleRegs : 1];
 };
 
-template <int MODE, int HALF>
-__device__ __forceinline__ Info<MODE, HALF> row_info(const Params& p, const Work& k, int t, int lane, int hh) {
-  using S = Shape<MODE, HALF>;
-  using I = Info<MODE, HALF>;
+template <int MODE, int HALF, bool PAIR>
+__device__ __forceinline__ Info<MODE, HALF, PAIR> row_info(const Params& p, const Work& k, int t, int lane, int hh) {
+  using S = Shape<MODE, HALF, PAIR>;
+  using I = Info<MODE, HALF, PAIR>;
   I r;
   if constexpr (!S::kIsDw) {
     const bool in = t < k.padded;
@@ -474,9 +539,32 @@ __device__ __forceinline__ Info<MODE, HALF> row_info(const Params& p, const Work
   return r;
 }
 
-template <int MODE, int HALF>
-__device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t tmem, const CUtensorMap* m_out) {
-  using S = Shape<MODE, HALF>;
+// A warp is done with an accumulator: the MMA thread (of CTA 0) waits for all of them.
+template <bool PAIR>
+__device__ __forceinline__ void release(uint64_t* bar) {
+  if constexpr (PAIR)
+    mbar_arrive_leader(bar);
+  else
+    mbar_arrive(bar);
+}
+
+// The part of a tile that this CTA of a pair holds.
+template <bool DW>
+__device__ __forceinline__ Work part_of(Work k, int rank) {
+  if (DW) {
+    k.m0 += rank * kTileRows;
+  } else {
+    k.row += rank * kTileRows;
+    k.n = max(0, min(kTileRows, k.n - rank * kTileRows));
+    k.padded = max(0, min(kTileRows, k.padded - rank * kTileRows));
+  }
+  return k;
+}
+
+template <int MODE, int HALF, bool PAIR>
+__device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t tmem, const CUtensorMap* m_out,
+                         int rank) {
+  using S = Shape<MODE, HALF, PAIR>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sp = warp & 3, hh = (warp - 4) >> 2;
   const int t = sp * 32 + lane;  // this thread's row of the tile
@@ -484,24 +572,24 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
   const uint32_t scales = smem_u32(smem + S::kOffScale) + (warp - 4) * kScales * 4;
   const uint32_t stage = smem_u32(smem + S::kOffOut) + (warp - 4) * kStageOut;
   RingPos d;
-  Info<MODE, HALF> info;
+  Info<MODE, HALF, PAIR> info;
   const uint32_t tops = smem_u32(smem + S::kOffTop);  // two tiles' [2][128] largest magnitudes
   int parity = 0;
   const bool small = p.k1 <= (1 << 22) / (128 * 128);
-  for (Cursor<S::kIsDw> at(p, S::kBN); !at.done(); at.next(p)) {
-    const Work k = at.cur;
+  for (Cursor<S, PAIR> at(p); !at.done(); at.next(p)) {
+    const Work k = PAIR ? part_of<S::kIsDw>(at.cur, rank) : at.cur;
     const bool empty = S::kIsDw && k.padded == 0;
     const int row = k.row + t;
-    if (at.w == (int)blockIdx.x) info = row_info<MODE, HALF>(p, k, t, lane, hh);
+    if (at.w == at.first()) info = row_info<MODE, HALF, PAIR>(p, k, t, lane, hh);
     const float row_factor = info.factor;
     const int slot = info.slot;
     if constexpr (S::kEight) {
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < Info<MODE, HALF>::kScaleRegs; ++i) st_shared_f32(scales + (32 * i + lane) * 4, info.scale[i]);
+      for (int i = 0; i < Info<MODE, HALF, PAIR>::kScaleRegs; ++i) st_shared_f32(scales + (32 * i + lane) * 4, info.scale[i]);
       __syncwarp();
     }
-    if (at.more()) info = row_info<MODE, HALF>(p, at.nxt, t, lane, hh);  // used a tile from now
+    if (at.more()) info = row_info<MODE, HALF, PAIR>(p, PAIR ? part_of<S::kIsDw>(at.nxt, rank) : at.nxt, t, lane, hh);  // used a tile from now
     if (!empty) {
       if (!bounded_wait(&b.acc_full[d.i], d.phase, b.abort_flag, p.status)) break;
       tc_fence_after();
@@ -509,7 +597,7 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
     const uint32_t acc = tmem + lanes + d.i * S::kAccStride;
     if (!S::kIsDw && sp * 32 >= k.padded) {  // none of this warp's rows is in the tile
       __syncwarp();
-      if (lane == 0) mbar_arrive(&b.acc_empty[d.i]);
+      if (lane == 0) release<PAIR>(&b.acc_empty[d.i]);
       d.next(S::kAccs);
       continue;
     }
@@ -524,7 +612,7 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
       reg_fence<32>(vb);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&b.acc_empty[d.i]);
+      if (lane == 0) release<PAIR>(&b.acc_empty[d.i]);
       float top = 0.f;
       float4 sa, sb;
       const int width = min(32, p.s - hh * 32);  // of this half: 32, 16 or none
@@ -571,7 +659,7 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
         if (c + 32 >= HALF / 2) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&b.acc_empty[d.i]);
+          if (lane == 0) release<PAIR>(&b.acc_empty[d.i]);
         }
         const int g0 = k.c0 + col;
 #pragma unroll
@@ -617,7 +705,7 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
         if (c + 32 >= HALF / 2) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&b.acc_empty[d.i]);
+          if (lane == 0) release<PAIR>(&b.acc_empty[d.i]);
         }
         const int g0 = k.c0 + col;
         if (t >= k.padded) continue;
@@ -668,7 +756,7 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
           if (last && !empty) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&b.acc_empty[d.i]);
+            if (lane == 0) release<PAIR>(&b.acc_empty[d.i]);
           }
           if constexpr (S::kIsDw) {
             if (lane == 0) bulk_wait_group_read<0>();  // the last store has read the staging
@@ -717,7 +805,7 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
         } else if (last && !empty) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&b.acc_empty[d.i]);
+          if (lane == 0) release<PAIR>(&b.acc_empty[d.i]);
         }
       }
     }
@@ -729,15 +817,16 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
   }
 }
 
-template <int MODE, int HALF>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int MODE, int HALF, bool PAIR>
+__global__ void __launch_bounds__(Shape<MODE, HALF, PAIR>::kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap m0, const __grid_constant__ CUtensorMap m1,
                    const __grid_constant__ CUtensorMap m2, const __grid_constant__ CUtensorMap m3, const Params p) {
-  using S = Shape<MODE, HALF>;
+  using S = Shape<MODE, HALF, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const Bars b = bars_at(smem + S::kOffBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = PAIR ? (int)cluster_ctarank() : 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&b.full[i], 1 + (S::kGathers ? kGatherWarps * 32 : 0));
@@ -745,37 +834,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < S::kAccs; ++i) {
       mbar_init(&b.acc_full[i], 1);
-      mbar_init(&b.acc_empty[i], kEpiWarps);
+      mbar_init(&b.acc_empty[i], PAIR ? 2 * kEpiWarps : kEpiWarps);
     }
     mbar_init(b.drain, 1);
     *b.abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(b.tmem_slot, S::kTmemCols);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(b.tmem_slot, S::kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(b.tmem_slot, S::kTmemCols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // the other CTA's barriers are used from here on
   tc_fence_after();
   const uint32_t tmem = *b.tmem_slot;
   if (warp == 0) {
-    box_loads<MODE, HALF>(p, b, smem, &m0, &m1, &m3);
+    box_loads<MODE, HALF, PAIR>(p, b, smem, &m0, &m1, &m2, &m3, rank);
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) mma_role<MODE, HALF>(p, b, smem, tmem);
+    if (lane == 0 && rank == 0) mma_role<MODE, HALF, PAIR>(p, b, smem, tmem);
     __syncwarp();
   } else if (warp < 4 || warp >= 12) {
-    if constexpr (S::kGathers) row_copies<MODE, HALF>(p, b, smem, warp < 4 ? warp - 2 : warp - 10);
+    if constexpr (S::kGathers) row_copies<MODE, HALF, PAIR>(p, b, smem, warp < 4 ? warp - 2 : warp - 10);
     __syncwarp();
   } else {
-    epilogue<MODE, HALF>(p, b, smem, tmem, &m2);
+    epilogue<MODE, HALF, PAIR>(p, b, smem, tmem, &m2, rank);
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // neither CTA leaves while the other's MMAs or arrivals may reach it
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, S::kTmemCols);
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem, S::kTmemCols);
+    else
+      tmem_dealloc(tmem, S::kTmemCols);
   }
 }
 
@@ -811,25 +910,37 @@ bool make_map(CUtensorMap* m, const void* base, int bytes, int64_t width, int64_
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, int HALF>
+template <int MODE, int HALF, bool PAIR>
 cudaError_t launch(const ExpertsArgs& a, Params p, int64_t items, const CUtensorMap& m0, const CUtensorMap& m1,
                    const CUtensorMap& m2, const CUtensorMap& m3) {
-  using S = Shape<MODE, HALF>;
+  using S = Shape<MODE, HALF, PAIR>;
   static_assert(S::kSmem <= 227 * 1024, "shared memory");
   int dev = 0, sms = 148;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   static std::atomic<int> done[64] = {};
   if (dev < 0 || dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(grouped_kernel<MODE, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    e = cudaFuncSetAttribute(grouped_kernel<MODE, HALF, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)S::kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev].store(1, std::memory_order_release);
   }
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   p.status = a.status;
-  const int grid = (int)(items < sms ? items : sms);
-  grouped_kernel<MODE, HALF><<<grid, kThreads, S::kSmem, a.stream>>>(m0, m1, m2, m3, p);
-  return cudaGetLastError();
+  constexpr int ctas = PAIR ? 2 : 1;
+  const int64_t most = sms / ctas;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((items < most ? items : most) * ctas));
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, grouped_kernel<MODE, HALF, PAIR>, m0, m1, m2, m3, p);
 }
 
 int tiles_of(int n, int bn) { return (n + bn - 1) / bn; }
@@ -842,10 +953,10 @@ int tiles_of(int n, int bn) { return (n + bn - 1) / bn; }
 #define MORE_MAP(...) \
   if (!make_map(__VA_ARGS__)) return cudaErrorInvalidValue
 
-// H = silu(X A^T) * (X B^T); x_bytes: 2 for bf16, 1 for 8 bits
+// H = silu(X A^T) * (X B^T).  pair: X holds the rows already picked, [R][h].
 template <int MODE>
 cudaError_t run_up(const ExpertsArgs& a, const Rows& rows, const void* X, const float* x_scale, void* H,
-                   float* h_scale = nullptr) {
+                   float* h_scale, bool pair) {
   constexpr int bytes = MODE == kUp8 ? 1 : 2, box = 128 / bytes;
   Params p = {};
   p.rows = rows;
@@ -858,18 +969,22 @@ cudaError_t run_up(const ExpertsArgs& a, const Rows& rows, const void* X, const 
   p.out_scale = h_scale;
   p.col_scale = a.up_scale;
   p.X = X;
-  CUtensorMap m1;
+  CUtensorMap m0, m1;
   // 128 + 128 columns a tile; 64 + 64 where the expert has no more
   const int half = a.s <= 64 ? 64 : 128;
   MORE_MAP(&m1, a.W_up, bytes, a.h, 2 * (int64_t)a.s, a.M, box, half);
   p.nc = tiles_of(a.s, half);
-  const int64_t items = max_tiles(a.S(), a.M) * p.nc;
-  if (half == 64) return launch<MODE, 64>(a, p, items, m1, m1, m1, m1);
-  return launch<MODE, 128>(a, p, items, m1, m1, m1, m1);
+  const int64_t items = max_tiles(a.S(), a.M, pair ? 2 * kTileRows : kTileRows) * p.nc;
+  if (pair) {
+    MORE_MAP(&m0, X, bytes, a.h, max_rows(a.S(), a.M), 0, box, kTileRows);
+    return launch<MODE, 128, true>(a, p, items, m0, m1, m1, m1);
+  }
+  if (half == 64) return launch<MODE, 64, false>(a, p, items, m1, m1, m1, m1);
+  return launch<MODE, 128, false>(a, p, items, m1, m1, m1, m1);
 }
 
 template <int MODE>
-cudaError_t run_down(const ExpertsArgs& a, const Rows& rows, const void* H, const float* h_scale, void* Y) {
+cudaError_t run_down(const ExpertsArgs& a, const Rows& rows, const void* H, const float* h_scale, void* Y, bool pair) {
   constexpr int bytes = MODE == kDown8 ? 1 : 2, box = 128 / bytes;
   Params p = {};
   p.rows = rows;
@@ -883,8 +998,9 @@ cudaError_t run_down(const ExpertsArgs& a, const Rows& rows, const void* H, cons
   p.nc = tiles_of(a.h, 256);
   CUtensorMap m0, m1;
   MORE_MAP(&m0, H, bytes, a.s, max_rows(a.S(), a.M), 0, box, kTileRows);
-  MORE_MAP(&m1, a.W_down, bytes, a.s, a.h, a.M, box, 256);
-  return launch<MODE, 64>(a, p, max_tiles(a.S(), a.M) * p.nc, m0, m1, m0, m0);
+  MORE_MAP(&m1, a.W_down, bytes, a.s, a.h, a.M, box, pair ? 128 : 256);
+  const int64_t items = max_tiles(a.S(), a.M, pair ? 2 * kTileRows : kTileRows) * p.nc;
+  return pair ? launch<MODE, 64, true>(a, p, items, m0, m1, m0, m0) : launch<MODE, 64, false>(a, p, items, m0, m1, m0, m0);
 }
 
 }  // namespace experts
@@ -896,6 +1012,7 @@ namespace {
 struct Buffers {
   Rows rows;
   void *H, *Hq, *Xq, *Y;
+  void *Xr, *Dr;  // X's (or its 8 bits') and y_bar's rows in the padded layout, for CTA pairs
   float *x_scale, *h_scale, *part;
   __nv_bfloat16 *pre, *mid;
   size_t bytes;
@@ -905,20 +1022,31 @@ enum Kind { kForward = 0, kInt8 = 1, kBackward = 2 };
 
 int gate_parts(int s) { return s <= 64 ? 2 : (s + 127) / 128 * 2; }
 
+// CTA pairs with 256-row tiles, the rows picked by token copied together first.  For wide experts with enough rows to
+// fill such tiles; narrow ones read each picked row once anyway, and are bound by memory.
+bool takes_pairs(int64_t S, int s, int M) { return s > 128 && S >= 192 * (int64_t)M; }
+
 Buffers carve(void* scratch, int64_t N, int h, int s, int M, int k, int kind) {
   Buffers b = {};
   Carver c(scratch);
   const int64_t S = N * k, R = max_rows(S, M);
+  const bool pair = takes_pairs(S, s, M);
   b.rows = carve_rows(c, S, M);
   if (kind == kForward) {
+    if (pair) b.Xr = c.take<__nv_bfloat16>(R * h);
     b.H = c.take<__nv_bfloat16>(R * s);
   } else if (kind == kInt8) {
     b.Xq = c.take<int8_t>(N * h);
     b.x_scale = c.take<float>(N);
+    if (pair) b.Xr = c.take<int8_t>(R * h);
     if (s > 64) b.H = c.take<float>(R * s);
     b.Hq = c.take<int8_t>(R * s);
     b.h_scale = c.take<float>(R);
   } else {
+    if (pair) {
+      b.Xr = c.take<__nv_bfloat16>(R * h);
+      b.Dr = c.take<__nv_bfloat16>(R * h);
+    }
     b.pre = c.take<__nv_bfloat16>(R * 2 * s);
     b.mid = c.take<__nv_bfloat16>(R * s);
     b.part = c.take<float>(R * gate_parts(s));
@@ -936,33 +1064,44 @@ size_t experts_scratch(int64_t N, int h, int s, int M, int k, int kind) {
 
 cudaError_t launch_experts(const ExpertsArgs& a) {
   const Buffers b = carve(a.scratch, a.N, a.h, a.s, a.M, a.k, kForward);
-  MORE_TRY(launch_rows(a, b.rows));
-  MORE_TRY(run_up<kUp>(a, b.rows, a.X, nullptr, b.H));
-  MORE_TRY(run_down<kDown>(a, b.rows, b.H, nullptr, b.Y));
+  const bool pair = takes_pairs(a.S(), a.s, a.M);
+  MORE_TRY(launch_rows(a, b.rows, pair ? 2 * kTileRows : kTileRows));
+  if (pair) MORE_TRY(launch_pick(a, b.rows, a.X, 2 * a.h, b.Xr));
+  MORE_TRY(run_up<kUp>(a, b.rows, pair ? b.Xr : a.X, nullptr, b.H, nullptr, pair));
+  MORE_TRY(run_down<kDown>(a, b.rows, b.H, nullptr, b.Y, pair));
   return launch_combine(a, b.rows, static_cast<const __nv_bfloat16*>(b.Y), a.out);
 }
 
 cudaError_t launch_experts_int8(const ExpertsArgs& a) {
   const Buffers b = carve(a.scratch, a.N, a.h, a.s, a.M, a.k, kInt8);
-  MORE_TRY(launch_rows(a, b.rows));
+  const bool pair = takes_pairs(a.S(), a.s, a.M);
+  MORE_TRY(launch_rows(a, b.rows, pair ? 2 * kTileRows : kTileRows));
   MORE_TRY(launch_quantize_bf16(static_cast<const __nv_bfloat16*>(a.X), a.N, a.h, static_cast<int8_t*>(b.Xq),
                                 b.x_scale, a.stream));
+  if (pair) MORE_TRY(launch_pick(a, b.rows, b.Xq, a.h, b.Xr));
   if (a.s <= 64) {  // one tile holds the middle of an expert's rows: rounded to 8 bits in the product's epilogue
-    MORE_TRY(run_up<kUp8>(a, b.rows, b.Xq, b.x_scale, b.Hq, b.h_scale));
+    MORE_TRY(run_up<kUp8>(a, b.rows, b.Xq, b.x_scale, b.Hq, b.h_scale, false));
   } else {
-    MORE_TRY(run_up<kUp8>(a, b.rows, b.Xq, b.x_scale, b.H));
+    MORE_TRY(run_up<kUp8>(a, b.rows, pair ? b.Xr : b.Xq, b.x_scale, b.H, nullptr, pair));
     MORE_TRY(launch_quantize_rows(a, b.rows, static_cast<const float*>(b.H), a.s, static_cast<int8_t*>(b.Hq),
-                                  b.h_scale));
+                                  b.h_scale, pair ? 2 * kTileRows : kTileRows));
   }
-  MORE_TRY(run_down<kDown8>(a, b.rows, b.Hq, b.h_scale, b.Y));
+  MORE_TRY(run_down<kDown8>(a, b.rows, b.Hq, b.h_scale, b.Y, pair));
   return launch_combine(a, b.rows, static_cast<const __nv_bfloat16*>(b.Y), a.out);
 }
 
 cudaError_t launch_experts_backward(const ExpertsArgs& a) {
   const Buffers b = carve(a.scratch, a.N, a.h, a.s, a.M, a.k, kBackward);
   const int64_t S = a.S(), R = max_rows(S, a.M);
-  MORE_TRY(launch_rows(a, b.rows));
-  CUtensorMap m1, m2, m3;
+  const bool pair = takes_pairs(S, a.s, a.M);
+  const int rows = pair ? 2 * kTileRows : kTileRows;
+  const int64_t tiles = max_tiles(S, a.M, rows);
+  MORE_TRY(launch_rows(a, b.rows, rows));
+  if (pair) {
+    MORE_TRY(launch_pick(a, b.rows, a.X, 2 * a.h, b.Xr));
+    MORE_TRY(launch_pick(a, b.rows, a.out_bar, 2 * a.h, b.Dr));
+  }
+  CUtensorMap m0, m1, m2, m3;
   Params p = {};
   p.rows = b.rows;
   p.R = R;
@@ -982,8 +1121,15 @@ cudaError_t launch_experts_backward(const ExpertsArgs& a) {
     q.nc = tiles_of(a.s, half);
     MORE_MAP(&m1, a.W_up, 2, a.h, 2 * (int64_t)a.s, a.M, 64, half);
     MORE_MAP(&m3, a.W_down, 2, a.s, a.h, a.M, 64, 64);
-    MORE_TRY((half == 64 ? launch<kBack, 64>(a, q, max_tiles(S, a.M) * q.nc, m1, m1, m1, m3)
-                         : launch<kBack, 128>(a, q, max_tiles(S, a.M) * q.nc, m1, m1, m1, m3)));
+    if (pair) {
+      MORE_MAP(&m0, b.Xr, 2, a.h, R, 0, 64, kTileRows);
+      MORE_MAP(&m2, b.Dr, 2, a.h, R, 0, 64, kTileRows);
+      MORE_TRY((launch<kBack, 128, true>(a, q, tiles * q.nc, m0, m1, m2, m3)));
+    } else if (half == 64) {
+      MORE_TRY((launch<kBack, 64, false>(a, q, tiles * q.nc, m1, m1, m1, m3)));
+    } else {
+      MORE_TRY((launch<kBack, 128, false>(a, q, tiles * q.nc, m1, m1, m1, m3)));
+    }
   }
   {
     Params q = p;
@@ -991,29 +1137,40 @@ cudaError_t launch_experts_backward(const ExpertsArgs& a) {
     q.cols = a.h;
     q.out = b.Y;
     q.nc = tiles_of(a.h, 256);
-    MORE_MAP(&m1, b.pre, 2, 2 * (int64_t)a.s, R, 0, 64, kTileRows);
-    MORE_MAP(&m2, a.W_up, 2, a.h, 2 * (int64_t)a.s, a.M, 64, 64);
-    MORE_TRY((launch<kDx, 64>(a, q, max_tiles(S, a.M) * q.nc, m1, m2, m1, m1)));
+    MORE_MAP(&m0, b.pre, 2, 2 * (int64_t)a.s, R, 0, 64, kTileRows);
+    MORE_MAP(&m1, a.W_up, 2, a.h, 2 * (int64_t)a.s, a.M, 64, 64);
+    MORE_TRY((pair ? launch<kDx, 64, true>(a, q, tiles * q.nc, m0, m1, m0, m0)
+                   : launch<kDx, 64, false>(a, q, tiles * q.nc, m0, m1, m0, m0)));
   }
   {
     Params q = p;
     q.cols = a.h;
     q.nc = tiles_of(a.h, 256);
-    q.nm = tiles_of(2 * a.s, kTileRows);
+    q.nm = tiles_of(2 * a.s, rows);
     q.items = a.M * q.nm * q.nc;
-    MORE_MAP(&m1, b.pre, 2, 2 * (int64_t)a.s, R, 0, 64, 64);
+    MORE_MAP(&m0, b.pre, 2, 2 * (int64_t)a.s, R, 0, 64, 64);
     MORE_MAP(&m2, a.W_up_bar, 2, a.h, 2 * (int64_t)a.s, a.M, 64, 32);
-    MORE_TRY((launch<kDwUp, 64>(a, q, q.items, m1, m1, m2, m1)));
+    if (pair) {
+      MORE_MAP(&m1, b.Xr, 2, a.h, R, 0, 64, 64);
+      MORE_TRY((launch<kDwUp, 64, true>(a, q, q.items, m0, m1, m2, m0)));
+    } else {
+      MORE_TRY((launch<kDwUp, 64, false>(a, q, q.items, m0, m0, m2, m0)));
+    }
   }
   {
     Params q = p;
     q.cols = a.s;
     q.nc = tiles_of(a.s, 256);
-    q.nm = tiles_of(a.h, kTileRows);
+    q.nm = tiles_of(a.h, rows);
     q.items = a.M * q.nm * q.nc;
     MORE_MAP(&m1, b.mid, 2, a.s, R, 0, 64, 64);
     MORE_MAP(&m2, a.W_down_bar, 2, a.s, a.h, a.M, 64, 32);
-    MORE_TRY((launch<kDwDown, 64>(a, q, q.items, m1, m1, m2, m1)));
+    if (pair) {
+      MORE_MAP(&m0, b.Dr, 2, a.h, R, 0, 64, 64);
+      MORE_TRY((launch<kDwDown, 64, true>(a, q, q.items, m0, m1, m2, m0)));
+    } else {
+      MORE_TRY((launch<kDwDown, 64, false>(a, q, q.items, m1, m1, m2, m1)));
+    }
   }
   MORE_TRY(launch_gate_grads(a, b.rows, b.part, gate_parts(a.s), R));
   return launch_combine(a, b.rows, static_cast<const __nv_bfloat16*>(b.Y), a.out);

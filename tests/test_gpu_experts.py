@@ -12,10 +12,12 @@ SIZES = [  # N, h, s, M, k
     (1, 8, 8, 8, 1), (1, 64, 16, 8, 8), (2, 2048, 64, 64, 8), (37, 72, 24, 16, 3), (300, 136, 200, 8, 2),
     (130, 520, 64, 40, 5), (1000, 256, 72, 24, 4), (129, 64, 264, 1, 1), (513, 320, 136, 3, 2), (700, 1096, 392, 8, 3),
     (64, 128, 64, 1000, 16),
+    (260, 1024, 160, 1, 1), (1500, 264, 1032, 4, 2), (3000, 200, 136, 16, 3),  # wide experts with many rows: CTA pairs
 ]
 SIZES_8 = [  # the same with h and s in whole 16s
     (1, 16, 16, 8, 1), (1, 64, 16, 8, 8), (2, 2048, 64, 64, 8), (37, 80, 48, 16, 3), (300, 144, 208, 8, 2),
     (130, 528, 64, 40, 5), (129, 64, 272, 1, 1), (513, 320, 144, 3, 2), (700, 1104, 400, 8, 3), (64, 128, 64, 1000, 16),
+    (260, 1024, 160, 1, 1), (1500, 272, 1040, 4, 2), (3000, 208, 144, 16, 3),
 ]
 
 
