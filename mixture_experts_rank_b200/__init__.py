@@ -276,14 +276,49 @@ def dispatch(idx: torch.Tensor, M: int, *, scratch: torch.Tensor | None = None, 
     return out_offsets, out_sorted
 
 
+class _Here:
+    """The context of a call on the current device and its current stream: none."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+class _There:
+    """The context of a call on another device or stream than the current one."""
+
+    def __init__(self, device, stream):
+        self.parts = torch.cuda.device(device), torch.cuda.stream(stream)
+
+    def __enter__(self):
+        for p in self.parts:
+            p.__enter__()
+
+    def __exit__(self, *exc):
+        for p in reversed(self.parts):
+            p.__exit__(*exc)
+        return False
+
+
+_HERE = _Here()
+
+
 def _on_device(first: torch.Tensor, stream, **tensors):
-    """Checks that every tensor lies on the device of ``first``, and gives that device's context and stream."""
+    """Checks that every tensor lies on the device of ``first``; the context in which the call runs there, on the given
+    stream or that device's current one."""
+    device = first.device
     for name, t in tensors.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, X on {first.device}")
-    if stream is not None and stream.device != first.device:
-        raise ValueError(f"the stream is on {stream.device}, X on {first.device}")
-    return torch.cuda.device(first.device), torch.cuda.current_stream(first.device) if stream is None else stream
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, {device} was expected")
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return _HERE
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, {device} was expected")
+    return _There(device, stream)
 
 
 def _typed(t, name, dtype, shape):
@@ -334,13 +369,13 @@ def experts(X: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tensor, gate: tor
     ``offsets, slots`` from :func:`dispatch`.  Returns bf16 [N, h].  h and s are multiples of 8.
     """
     N, h, s, M, k = _expert_shapes(X, W_up, W_down, gate, offsets, slots, torch.bfloat16)
-    device, stream = _on_device(X, stream, W_up=W_up, W_down=W_down, gate=gate, offsets=offsets, slots=slots, out=out,
+    context = _on_device(X, stream, W_up=W_up, W_down=W_down, gate=gate, offsets=offsets, slots=slots, out=out,
                                 scratch=scratch)
-    with device, torch.cuda.stream(stream):
+    with context:
         out = _output(out, "out", torch.bfloat16, (N, h), X.device)
         scratch = _scratch(scratch, experts_scratch_bytes(N, h, s, M, k), X.device)
         st = _lib.more_experts(_ptr(X), _ptr(W_up), _ptr(W_down), N, h, s, M, k, _ptr(gate), _ptr(offsets),
-                               _ptr(slots), _ptr(out), _ptr(scratch), scratch.numel(), _stream_handle(stream))
+                               _ptr(slots), _ptr(out), _ptr(scratch), scratch.numel(), _stream_handle(None))
     _check(st, "more_experts")
     return out
 
@@ -352,13 +387,13 @@ def quantize_rows(V: torch.Tensor, *, out_q=None, out_scale=None, stream=None) -
     V = _as_bf16(V, "V")
     if V.dim() < 1:
         raise ValueError("V must have rows")
-    device, stream = _on_device(V, stream, out_q=out_q, out_scale=out_scale)
-    with device, torch.cuda.stream(stream):
+    context = _on_device(V, stream, out_q=out_q, out_scale=out_scale)
+    with context:
         out_q = _output(out_q, "out_q", torch.int8, V.shape, V.device)
         out_scale = _output(out_scale, "out_scale", torch.float32, V.shape[:-1], V.device)
         width = V.shape[-1]
         st = _lib.more_quantize_rows(_ptr(V), V.numel() // max(width, 1), width, _ptr(out_q), _ptr(out_scale),
-                                     _stream_handle(stream))
+                                     _stream_handle(None))
     _check(st, "more_quantize_rows")
     return out_q, out_scale
 
@@ -376,14 +411,14 @@ def experts_int8(X: torch.Tensor, W_up: torch.Tensor, up_scale: torch.Tensor, W_
     N, h, s, M, k = _expert_shapes(X, W_up, W_down, gate, offsets, slots, torch.int8)
     _typed(up_scale, "up_scale", torch.float32, (M, 2 * s))
     _typed(down_scale, "down_scale", torch.float32, (M, h))
-    device, stream = _on_device(X, stream, W_up=W_up, up_scale=up_scale, W_down=W_down, down_scale=down_scale, gate=gate,
+    context = _on_device(X, stream, W_up=W_up, up_scale=up_scale, W_down=W_down, down_scale=down_scale, gate=gate,
                                 offsets=offsets, slots=slots, out=out, scratch=scratch)
-    with device, torch.cuda.stream(stream):
+    with context:
         out = _output(out, "out", torch.bfloat16, (N, h), X.device)
         scratch = _scratch(scratch, experts_int8_scratch_bytes(N, h, s, M, k), X.device)
         st = _lib.more_experts_int8(_ptr(X), _ptr(W_up), _ptr(up_scale), _ptr(W_down), _ptr(down_scale), N, h, s, M, k,
                                     _ptr(gate), _ptr(offsets), _ptr(slots), _ptr(out), _ptr(scratch), scratch.numel(),
-                                    _stream_handle(stream))
+                                    _stream_handle(None))
     _check(st, "more_experts_int8")
     return out
 
@@ -402,11 +437,11 @@ def experts_backward(X: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tensor, 
     :func:`route_backward`, which adds the router's share of the X gradient."""
     N, h, s, M, k = _expert_shapes(X, W_up, W_down, gate, offsets, slots, torch.bfloat16)
     _typed(out_bar, "out_bar", torch.bfloat16, (N, h))
-    device, stream = _on_device(X, stream, W_up=W_up, W_down=W_down, gate=gate, offsets=offsets, slots=slots,
+    context = _on_device(X, stream, W_up=W_up, W_down=W_down, gate=gate, offsets=offsets, slots=slots,
                                 out_bar=out_bar, out_Xbar=out_Xbar, out_W_up_bar=out_W_up_bar,
                                 out_W_down_bar=out_W_down_bar, out_gate_bar=out_gate_bar, out_logits_bar=out_logits_bar,
                                 scratch=scratch)
-    with device, torch.cuda.stream(stream):
+    with context:
         bf16, f32 = torch.bfloat16, torch.float32
         outs = (_output(out_Xbar, "out_Xbar", bf16, (N, h), X.device),
                 _output(out_W_up_bar, "out_W_up_bar", bf16, W_up.shape, X.device),
@@ -416,7 +451,7 @@ def experts_backward(X: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tensor, 
         scratch = _scratch(scratch, experts_backward_scratch_bytes(N, h, s, M, k), X.device)
         st = _lib.more_experts_backward(_ptr(X), _ptr(W_up), _ptr(W_down), N, h, s, M, k, _ptr(gate), _ptr(offsets),
                                         _ptr(slots), _ptr(out_bar), *(_ptr(t) for t in outs), _ptr(scratch),
-                                        scratch.numel(), _stream_handle(stream))
+                                        scratch.numel(), _stream_handle(None))
     _check(st, "more_experts_backward")
     return outs
 
@@ -443,15 +478,14 @@ def _layer_shapes(X, R1, R2, W_up, W_down, dtype):
 
 def moe_layer(X: torch.Tensor, R1: torch.Tensor, R2: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tensor, k: int, *,
               out=None, scratch: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """The whole layer: :func:`route` and the selected :func:`experts`, for a few tokens (N <= 64) the experts in one
-    kernel.  Weights as for :func:`experts`.  Returns bf16 [N, h]."""
+    """The whole layer: :func:`route` and the selected :func:`experts`, for a few tokens (N <= 64) in one kernel.  Weights as for :func:`experts`.  Returns bf16 [N, h]."""
     N, h, r, s, M = _layer_shapes(X, R1, R2, W_up, W_down, torch.bfloat16)
-    device, stream = _on_device(X, stream, R1=R1, R2=R2, W_up=W_up, W_down=W_down, out=out, scratch=scratch)
-    with device, torch.cuda.stream(stream):
+    context = _on_device(X, stream, R1=R1, R2=R2, W_up=W_up, W_down=W_down, out=out, scratch=scratch)
+    with context:
         out = _output(out, "out", torch.bfloat16, (N, h), X.device)
         scratch = _scratch(scratch, moe_layer_scratch_bytes(N, h, s, M, k), X.device)
         st = _lib.more_moe_layer(_ptr(X), _ptr(R1), _ptr(R2), _ptr(W_up), _ptr(W_down), N, h, r, s, M, k, _ptr(out),
-                                 _ptr(scratch), scratch.numel(), _stream_handle(stream))
+                                 _ptr(scratch), scratch.numel(), _stream_handle(None))
     _check(st, "more_moe_layer")
     return out
 
@@ -463,14 +497,14 @@ def moe_layer_int8(X: torch.Tensor, R1: torch.Tensor, R2: torch.Tensor, W_up: to
     N, h, r, s, M = _layer_shapes(X, R1, R2, W_up, W_down, torch.int8)
     _typed(up_scale, "up_scale", torch.float32, (M, 2 * s))
     _typed(down_scale, "down_scale", torch.float32, (M, h))
-    device, stream = _on_device(X, stream, R1=R1, R2=R2, W_up=W_up, up_scale=up_scale, W_down=W_down,
+    context = _on_device(X, stream, R1=R1, R2=R2, W_up=W_up, up_scale=up_scale, W_down=W_down,
                                 down_scale=down_scale, out=out, scratch=scratch)
-    with device, torch.cuda.stream(stream):
+    with context:
         out = _output(out, "out", torch.bfloat16, (N, h), X.device)
         scratch = _scratch(scratch, moe_layer_int8_scratch_bytes(N, h, s, M, k), X.device)
         st = _lib.more_moe_layer_int8(_ptr(X), _ptr(R1), _ptr(R2), _ptr(W_up), _ptr(up_scale), _ptr(W_down),
                                       _ptr(down_scale), N, h, r, s, M, k, _ptr(out), _ptr(scratch), scratch.numel(),
-                                      _stream_handle(stream))
+                                      _stream_handle(None))
     _check(st, "more_moe_layer_int8")
     return out
 

@@ -509,7 +509,7 @@ namespace {
 // dispatch and the grouped products.
 struct LayerBuffers {
   int32_t *idx, *counts, *offsets, *slots;
-  float *gate, *mid, *x_scale;
+  float *gate, *mid, *x_scale, *z, *logits;
   int8_t* Xq;
   unsigned int* barrier;
   void *dispatch, *experts;
@@ -522,15 +522,17 @@ LayerBuffers carve_layer(void* scratch, int64_t N, int h, int s, int M, int k, b
   const int64_t S = N * k;
   b.idx = c.take<int32_t>(S);
   b.gate = c.take<float>(S);
-  b.counts = c.take<int32_t>((int64_t)M + 64);  // the barrier's counter follows the counts: one memset for both
   if (layer_few_fits(N, h, k)) {
-    b.barrier = b.counts ? reinterpret_cast<unsigned int*>(b.counts) + (M + 31) / 32 * 32 : nullptr;
+    b.barrier = c.take<unsigned int>(1);
+    b.z = c.take<float>(N * 128);  // r <= 128
+    b.logits = c.take<float>(N * M);
     b.mid = c.take<float>(S * s);
     if (int8) {
       b.Xq = c.take<int8_t>(N * h);
       b.x_scale = c.take<float>(N);
     }
   } else {
+    b.counts = c.take<int32_t>(M);
     b.offsets = c.take<int32_t>((int64_t)M + 1);
     b.slots = c.take<int32_t>(S);
     b.dispatch_bytes = (size_t)dispatch_scratch_bytes(S, M);
@@ -566,14 +568,18 @@ more_status moe_layer(const void* X, const void* R1, const void* R2, const void*
                 : more_experts(X, W_up, W_down, N, h, s, M, k, b.gate, b.offsets, b.slots, out, b.experts,
                                b.experts_bytes, stream);
   }
-  RouteArgs a = make_args(X, R1, R2, N, h, r, M, k, b.idx, b.gate, b.counts, nullptr, stream);
-  a.status = status;
   FewArgs f = {};
   f.X = X;
+  f.R1 = R1;
+  f.R2 = R2;
   f.W_up = W_up;
   f.W_down = W_down;
   f.up_scale = up_scale;
   f.down_scale = down_scale;
+  f.Xq = b.Xq;
+  f.x_scale = b.x_scale;
+  f.z = b.z;
+  f.logits = b.logits;
   f.idx = b.idx;
   f.gate = b.gate;
   f.mid = b.mid;
@@ -581,20 +587,13 @@ more_status moe_layer(const void* X, const void* R1, const void* R2, const void*
   f.out = out;
   f.N = N;
   f.h = h;
+  f.r = r;
   f.s = s;
   f.M = M;
   f.k = k;
   f.status = status;
   f.stream = stream;
-  cudaError_t e = cudaMemsetAsync(b.counts, 0, sizeof(int32_t) * ((size_t)M + 64), stream);
-  if (e == cudaSuccess && int8) {
-    f.Xq = b.Xq;
-    f.x_scale = b.x_scale;
-    e = launch_quantize_bf16(static_cast<const __nv_bfloat16*>(X), N, h, b.Xq, b.x_scale, stream);
-  }
-  if (e == cudaSuccess) e = auto_variant(a) == MORE_VARIANT_CLUSTER ? launch_cluster(a) : launch_small_n(a);
-  if (e == cudaSuccess) e = launch_layer_few(f);
-  return e == cudaSuccess ? MORE_OK : MORE_ERR_CUDA;
+  return launch_layer_few(f) == cudaSuccess ? MORE_OK : MORE_ERR_CUDA;
 }
 
 more_status validate_layer(const void* X, const void* R1, const void* R2, const void* W_up, const float* up_scale,

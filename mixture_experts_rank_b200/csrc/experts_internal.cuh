@@ -117,20 +117,21 @@ cudaError_t launch_quantize_bf16(const __nv_bfloat16* v, int64_t rows, int width
 cudaError_t launch_quantize_rows(const ExpertsArgs& a, const Rows& r, const float* v, int width, int8_t* q,
                                  float* scale, int tile_rows);
 
-// The selected experts of a few tokens (moe_layer.cu).  Xq and the scales: 8-bit weights.
+// The whole layer of a few tokens (moe_layer.cu).  Xq and the scales: 8-bit weights.
 struct FewArgs {
-  const void* X;
-  const int8_t* Xq;
-  const float* x_scale;
+  const void *X, *R1, *R2;
+  int8_t* Xq;      // [N][h]
+  float* x_scale;  // [N]
   const void *W_up, *W_down;
   const float *up_scale, *down_scale;
-  const int32_t* idx;
-  const float* gate;
-  float* mid;             // [N k][s]
-  unsigned int* barrier;  // zeroed before the launch
+  float *z, *logits;  // [N][r], [N][M]
+  int32_t* idx;       // [N k]
+  float* gate;        // [N k]
+  float* mid;         // [N k][s]
+  unsigned int* barrier;
   void* out;
   int64_t N;
-  int h, s, M, k;
+  int h, r, s, M, k;
   unsigned int* status;
   cudaStream_t stream;
 };

@@ -1,21 +1,27 @@
-// The whole layer for a few tokens: after the routing kernel, one cooperative kernel runs the selected experts.
+// The whole layer for a few tokens, in one cooperative kernel.
 //
-// The time of such a call is the reading of the selected experts' weights, once each, so everything is laid out for
-// that: no tensor cores (a handful of rows an expert), every warp streams whole rows of weights.
-//   1. Every CTA groups the N k selections by expert, up to 8 selections a group (its own copy, from the same list).
-//   2. Up: a warp takes row i of A_e and of B_e and the group's tokens; m = silu(a) * b goes to scratch in fp32.
+// The time of such a call is the latency of its steps and the reading of the selected experts' weights, once each, so
+// everything is laid out for those: no tensor cores (a handful of rows an expert), every step spread over all CTAs with
+// a barrier over the grid behind it, every warp streaming whole rows of weights.
+//   1. z = x R1: a CTA takes 16 columns of a token's z, its warps parts of h.  With 8-bit weights other CTAs round x.
+//   2. The logits z R2: a warp takes 8 experts of a token, a lane one row of R2 (or r / 32 of them); the N x M logits of
+//      these few tokens go through scratch.
+//   3. A CTA takes a token's largest k logits and their softmax (for up to kSolo tokens every CTA does so itself, which
+//      saves a barrier).  Then every CTA groups the N k selections by expert, up to 8 a group: its own copy.
+//   4. Up: a warp takes row i of A_e and of B_e and the group's tokens; m = silu(a) * b goes to scratch in fp32.
 //      Where there are too few rows for the machine's warps, 2 to 8 warps share a row, each a part of h.
-//   3. A barrier over the grid: the second product needs whole rows of m.
-//   4. Down: every CTA owns h / CTAs output channels for all experts, so a token's k contributions meet in its
+//   5. Down: every CTA owns h / CTAs output channels for all experts, so a token's k contributions meet in its
 //      shared memory, and out[n] = sum_j gate * y is summed there in the order of j: no second pass over a row buffer,
 //      and no atomics on the result.
-// Everything stays in fp32 until the output.  With 8-bit weights the products are integer dot products (four a
-// instruction); m is rounded to 8 bits when it is read, with its row's largest magnitude found after the barrier.
+// z is carried as the bf16 pair of the routing kernels; all else stays in fp32 until the output.  With 8-bit weights
+// the products are integer dot products (four an instruction); m is rounded to 8 bits when it is read, with its row's
+// largest magnitude found after the barrier.
 #include <algorithm>
 #include <atomic>
 
 #include "experts_internal.cuh"
 #include "sm100_ptx.cuh"
+#include "warp_simt.cuh"
 
 namespace more {
 namespace {
@@ -28,18 +34,20 @@ constexpr uint32_t kSmemMost = 200 * 1024;
 constexpr int kRowBlocks = 4;  // rows (times 32 / lanes a row) that a warp carries in the second product
 
 struct LayerArgs {
-  const __nv_bfloat16* X;
-  const int8_t* Xq;       // int8: X in 8 bits, and its scales
-  const float* x_scale;
+  const __nv_bfloat16 *X, *R1, *R2;
+  int8_t* Xq;  // int8: X in 8 bits, and its scales
+  float* x_scale;
   const void *W_up, *W_down;
   const float *up_scale, *down_scale;
-  const int32_t* idx;
-  const float* gate;
-  float* mid;  // [S][s]
+  float* z;       // [N][r]
+  float* logits;  // [N][M]
+  int32_t* idx;   // [S]
+  float* gate;    // [S]
+  float* mid;     // [S][s]
   __nv_bfloat16* out;
   unsigned int* barrier;  // 0 at the start
   unsigned int* status;
-  int N, h, s, M, k, S;
+  int N, h, r, s, M, k, S;
 };
 
 // ---- shared memory: the groups, the selections' output channels ------------------------------------------------
@@ -49,6 +57,7 @@ struct Shared {
   int16_t* lead;       // [S] group of a leading selection
   int32_t* group_e;    // [S] expert of a group
   int32_t* group_n;    // [S] its selections
+  float* gate;         // [S]
   float* top;          // [S] largest |m| (int8)
   float* y;            // [S][R]
 };
@@ -56,7 +65,7 @@ struct Shared {
 __host__ __device__ inline uint32_t round16(uint32_t v) { return (v + 15) & ~15u; }
 
 __host__ __device__ inline uint32_t layer_smem(int S, int R) {
-  return round16(4 * S) * 4 + round16(2 * kGroup * S) + round16(2 * S) + round16(4 * S * R) + 16;
+  return round16(4 * S) * 5 + round16(2 * kGroup * S) + round16(2 * S) + round16(4 * S * R) + 16;
 }
 
 __device__ __forceinline__ Shared shared_at(uint8_t* p, int S, int R) {
@@ -66,6 +75,8 @@ __device__ __forceinline__ Shared shared_at(uint8_t* p, int S, int R) {
   r.group_e = reinterpret_cast<int32_t*>(p);
   p += round16(4 * S);
   r.group_n = reinterpret_cast<int32_t*>(p);
+  p += round16(4 * S);
+  r.gate = reinterpret_cast<float*>(p);
   p += round16(4 * S);
   r.top = reinterpret_cast<float*>(p);
   p += round16(4 * S);
@@ -90,6 +101,13 @@ __device__ __forceinline__ uint4 load_weights(const void* p) {
 __device__ __forceinline__ void widen(uint32_t u, float& lo, float& hi) {
   lo = __uint_as_float(u << 16);
   hi = __uint_as_float(u & 0xffff0000u);
+}
+
+__device__ __forceinline__ void widen8(uint4 v, float (&x)[8]) {
+  widen(v.x, x[0], x[1]);
+  widen(v.y, x[2], x[3]);
+  widen(v.z, x[4], x[5]);
+  widen(v.w, x[6], x[7]);
 }
 
 __device__ __forceinline__ void dot8(float& acc, uint4 w, const float* x) {
@@ -126,11 +144,158 @@ constexpr int log2_of() {
   return V == 1 ? 0 : 1 + log2_of<(V > 1 ? V / 2 : 1)>();
 }
 
+// Barrier number `turn` (from 1) over a cooperative grid; false once the wait has run out.
+__device__ bool grid_barrier(unsigned int* counter, unsigned turn, unsigned int* status, int* failed) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    atomicAdd(counter, 1u);
+    *failed = 0;
+    const long long t0 = clock64();
+    for (unsigned spin = 0;; ++spin) {
+      unsigned v;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+      if (v >= turn * gridDim.x) break;
+      if ((spin & 255u) == 255u && clock64() - t0 > 8000000000ll) {  // some 4 s
+        atomicOr(status, MORE_DEVERR_WAIT_TIMEOUT);
+        *failed = 1;
+        break;
+      }
+    }
+    __threadfence();
+  }
+  __syncthreads();
+  return *failed == 0;
+}
+
+// Step 1.  `part`: 16 sums a warp.
+__device__ void project_tokens(const LayerArgs& a, float (*part)[2 * kGroup]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, blocks = a.r / 16;
+  for (int u = blockIdx.x; u < a.N * blocks; u += gridDim.x) {
+    const int n = u / blocks, b = (u - n * blocks) * 16;
+    float v;
+    int i;
+    warp_partial_z16_strided(a.X + (size_t)n * a.h, a.R1, a.h, a.r, b, threadIdx.x, kThreads, lane, v, i);
+    if ((lane & 1) == 0) part[warp][i - b] = v;
+    __syncthreads();
+    if (threadIdx.x < 16) {
+      float z = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) z += part[w][threadIdx.x];
+      a.z[n * a.r + b + threadIdx.x] = split_bf16_pair(z);
+    }
+    __syncthreads();
+  }
+}
+
+// x in 8 bits, a token a CTA, from the last CTA down (the first have z to compute).
+__device__ void round_tokens(const LayerArgs& a, float* warp_tops) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int n = gridDim.x - 1 - blockIdx.x; n < a.N; n += gridDim.x) {
+    const uint4* src = reinterpret_cast<const uint4*>(a.X + (size_t)n * a.h);
+    float top = 0.f, x[8];
+    for (int c = threadIdx.x; c < a.h / 8; c += kThreads) {
+      widen8(src[c], x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if (lane == 0) warp_tops[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, warp_tops[w]);
+    const float div = top > 0.f ? top : 1.f, inv = __fdiv_rn(127.f, div);
+    for (int c = threadIdx.x; c < a.h / 8; c += kThreads) {
+      widen8(src[c], x);
+      uint32_t o[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i >> 2] |= (uint32_t)(uint8_t)round8(x[i], div, inv) << (8 * (i & 3));
+      reinterpret_cast<uint2*>(a.Xq + (size_t)n * a.h)[c] = make_uint2(o[0], o[1]);
+    }
+    if (threadIdx.x == 0) a.x_scale[n] = __fdiv_rn(top, 127.f);
+    __syncthreads();
+  }
+}
+
+// Step 2.
+__device__ void expert_logits(const LayerArgs& a) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int octets = a.M / 8, mine = (octets - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  for (int u = warp; u < mine * a.N; u += kWarps) {
+    const int j = u / a.N, n = u - j * a.N;
+    const int e0 = 8 * ((int)blockIdx.x + (int)gridDim.x * j);
+    uint4 w[4];
+    float zi[4], acc[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = lane + 32 * i;
+      const bool in = row < a.r;
+      w[i] = in ? __ldg(reinterpret_cast<const uint4*>(a.R2 + (size_t)row * a.M + e0)) : make_uint4(0, 0, 0, 0);
+      zi[i] = in ? a.z[n * a.r + row] : 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[q] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x[8];
+      widen8(w[i], x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) acc[q] = fmaf(zi[i], x[q], acc[q]);
+    }
+    const float v = reduce_scatter<8>(acc, lane);
+    if ((lane & 3) == 0) a.logits[(size_t)n * a.M + e0 + (lane >> 2)] = v;
+  }
+}
+
+// Step 3 for token n: its selections and gates at idx and gate (shared or global memory).
+template <int KCAP>
+__device__ void select_experts(const LayerArgs& a, int n, float (*pv)[KCAP], int (*pe)[KCAP], int32_t* idx,
+                               float* gate) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float* l = a.logits + (size_t)n * a.M;
+  TopList<KCAP> list;
+  list.init();
+  for (int e = threadIdx.x; e < a.M; e += 4 * kThreads) {
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = e + i * kThreads < a.M ? l[e + i * kThreads] : -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) list.insert(v[i], e + i * kThreads);
+  }
+  float v;
+  int e;
+  warp_merge_topk<KCAP>(list, a.k, lane, v, e);
+  if (lane < KCAP) {
+    pv[warp][lane] = v;
+    pe[warp][lane] = e;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    TopList<KCAP> all;
+    all.init();
+    for (int q = lane; q < kWarps * KCAP; q += 32)
+      if (q % KCAP < a.k) all.insert_any(pv[q / KCAP][q % KCAP], pe[q / KCAP][q % KCAP]);
+    warp_merge_topk<KCAP>(all, a.k, lane, v, e);
+    const float top = __shfl_sync(0xffffffffu, v, 0);
+    const float ex = lane < a.k ? expf(v - top) : 0.f;
+    float sum = ex;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane < a.k) {
+      idx[n * a.k + lane] = e;
+      gate[n * a.k + lane] = ex / sum;
+    }
+  }
+  __syncthreads();
+}
+
 // Groups the selections by expert, in their order; the number of groups.
-__device__ int group_selections(const LayerArgs& a, const Shared& sh, int* counts) {
+__device__ int group_selections(const LayerArgs& a, const Shared& sh, bool solo, int* counts) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < a.S; i += kThreads) {
-    const int e = a.idx[i];
+    const int e = solo ? sh.expert[i] : a.idx[i];
+    if (!solo) sh.gate[i] = a.gate[i];
     const bool ok = e >= 0 && e < a.M;
     if (!ok && blockIdx.x == 0) atomicOr(a.status, MORE_DEVERR_BAD_INPUT);
     sh.expert[i] = ok ? e : -1;
@@ -205,10 +370,7 @@ __device__ __forceinline__ float up_bf16(const LayerArgs& a, const uint8_t* ra, 
       for (int t = 0; t < TB; ++t) {
         const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.X + (size_t)tok[t] * a.h + col));
         float x[8];
-        widen(v.x, x[0], x[1]);
-        widen(v.y, x[2], x[3]);
-        widen(v.z, x[4], x[5]);
-        widen(v.w, x[6], x[7]);
+        widen8(v, x);
         dot8(acc[2 * t], wa[i], x);
         dot8(acc[2 * t + 1], wb[i], x);
       }
@@ -250,7 +412,7 @@ __device__ __forceinline__ float up_int8(const LayerArgs& a, const uint8_t* ra, 
       if (col >= a.h) break;
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.Xq + (size_t)tok[t] * a.h + col));
+        const uint4 x = *reinterpret_cast<const uint4*>(a.Xq + (size_t)tok[t] * a.h + col);  // written by this kernel
         acc[2 * t] = dot16(wa[i], x, acc[2 * t]);
         acc[2 * t + 1] = dot16(wb[i], x, acc[2 * t + 1]);
       }
@@ -369,30 +531,6 @@ __device__ void up_phase(const LayerArgs& a, const Shared& sh, int groups, float
   }
 }
 
-// Barrier over a cooperative grid; false once the wait has run out.
-__device__ bool grid_barrier(unsigned int* counter, unsigned int* status, int* failed) {
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    atomicAdd(counter, 1u);
-    *failed = 0;
-    const uint64_t t0 = sm100::global_timer_ns();
-    for (unsigned spin = 0;; ++spin) {
-      unsigned v;
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
-      if (v >= gridDim.x) break;
-      if ((spin & 1023u) == 1023u && sm100::global_timer_ns() - t0 > 4000000000ull) {
-        atomicOr(status, MORE_DEVERR_WAIT_TIMEOUT);
-        *failed = 1;
-        break;
-      }
-    }
-    __threadfence();
-  }
-  __syncthreads();
-  return *failed == 0;
-}
-
 // Rows r0 + rb * rows + lane / L (rb < kRowBlocks) of expert e for up to TB selections of group g.
 template <bool I8, int TB>
 __device__ __forceinline__ void down_unit(const LayerArgs& a, const Shared& sh, int g, int n, int o0, int R, int r0,
@@ -496,21 +634,38 @@ __device__ void down_phase(const LayerArgs& a, const Shared& sh, int groups, int
   for (int i = threadIdx.x; i < a.N * R; i += kThreads) {
     const int n = i / R, r = i - n * R;
     float sum = 0.f;
-    for (int j = 0; j < a.k; ++j) sum = fmaf(a.gate[n * a.k + j], sh.y[(n * a.k + j) * R + r], sum);
+    for (int j = 0; j < a.k; ++j) sum = fmaf(sh.gate[n * a.k + j], sh.y[(n * a.k + j) * R + r], sum);
     a.out[(size_t)n * a.h + o0 + r] = __float2bfloat16_rn(sum);
   }
 }
 
-template <bool I8>
+constexpr int kSolo = 2;
+
+template <bool I8, int KCAP>
 __global__ void __launch_bounds__(kThreads, 1) layer_kernel(const LayerArgs a, int rows_each) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float part[kWarps][2 * kGroup];
+  __shared__ float pv[kWarps][KCAP];
+  __shared__ int pe[kWarps][KCAP];
   __shared__ int counts[kWarps];
   __shared__ int failed;
   const Shared sh = shared_at(smem, a.S, rows_each);
-  const int groups = group_selections(a, sh, counts);
+  unsigned turn = 0;
+  project_tokens(a, part);
+  if constexpr (I8) round_tokens(a, &part[0][0]);
+  if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
+  expert_logits(a);
+  if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
+  const bool solo = a.N <= kSolo;
+  if (solo) {
+    for (int n = 0; n < a.N; ++n) select_experts<KCAP>(a, n, pv, pe, sh.expert, sh.gate);
+  } else {
+    for (int n = blockIdx.x; n < a.N; n += gridDim.x) select_experts<KCAP>(a, n, pv, pe, a.idx, a.gate);
+    if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
+  }
+  const int groups = group_selections(a, sh, solo, counts);
   up_phase<I8>(a, sh, groups, part);
-  if (!grid_barrier(a.barrier, a.status, &failed)) return;
+  if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
   down_phase<I8>(a, sh, groups, rows_each);
 }
 
@@ -521,7 +676,7 @@ int sm_count() {
   return sms;
 }
 
-template <bool I8>
+template <bool I8, int KCAP>
 cudaError_t launch_layer(const LayerArgs& a, cudaStream_t stream) {
   const int grid = sm_count();
   const int rows_each = (a.h + grid - 1) / grid;
@@ -531,7 +686,7 @@ cudaError_t launch_layer(const LayerArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   static std::atomic<int> done[64] = {};
   if (dev < 0 || dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(layer_kernel<I8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost);
+    e = cudaFuncSetAttribute(layer_kernel<I8, KCAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev].store(1, std::memory_order_release);
   }
@@ -541,11 +696,11 @@ cudaError_t launch_layer(const LayerArgs& a, cudaStream_t stream) {
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeCooperative;  // every CTA waits for the others at the barrier
+  attr[0].id = cudaLaunchAttributeCooperative;  // every CTA waits for the others at the barriers
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, layer_kernel<I8>, a, rows_each);
+  return cudaLaunchKernelEx(&cfg, layer_kernel<I8, KCAP>, a, rows_each);
 }
 
 }  // namespace
@@ -559,6 +714,11 @@ bool layer_few_fits(int64_t N, int h, int k) {
 cudaError_t launch_layer_few(const FewArgs& f) {
   LayerArgs a = {};
   a.X = static_cast<const __nv_bfloat16*>(f.X);
+  a.R1 = static_cast<const __nv_bfloat16*>(f.R1);
+  a.R2 = static_cast<const __nv_bfloat16*>(f.R2);
+  a.z = f.z;
+  a.logits = f.logits;
+  a.r = f.r;
   a.Xq = f.Xq;
   a.x_scale = f.x_scale;
   a.W_up = f.W_up;
@@ -577,7 +737,10 @@ cudaError_t launch_layer_few(const FewArgs& f) {
   a.M = f.M;
   a.k = f.k;
   a.S = (int)(f.N * f.k);
-  return f.Xq ? launch_layer<true>(a, f.stream) : launch_layer<false>(a, f.stream);
+  const cudaError_t e = cudaMemsetAsync(f.barrier, 0, sizeof(unsigned int), f.stream);
+  if (e != cudaSuccess) return e;
+  if (a.k <= 8) return f.Xq ? launch_layer<true, 8>(a, f.stream) : launch_layer<false, 8>(a, f.stream);
+  return f.Xq ? launch_layer<true, 16>(a, f.stream) : launch_layer<false, 16>(a, f.stream);
 }
 
 }  // namespace more
