@@ -387,8 +387,9 @@ more_status more_experts_backward(const void* X, const void* W_up, const void* W
 /*
  * The whole MoE layer (MoRE §2 "MoE layer"): more_route and then the selected experts, out = the `out` of more_experts
  * for the router's own selections and gates.  For a few tokens (N <= 64, decoding) everything runs in one kernel that
- * reads each selected expert's weights once and stays in fp32 up to the output (its logits are more_route's up to the
- * order of their sums); for more the call runs more_route, more_dispatch and more_experts.
+ * reads each selected expert's weights once; its logits are more_route's up to the order of their sums, and
+ * silu(A x) * (B x) is carried as a bf16 pair (about 16 bits) and the slots' rows in fp32.  For more the call runs
+ * more_route, more_dispatch and more_experts.
  * Arguments and requirements: those of more_route (X, R1, R2, r, k, M) and of more_experts (W_up, W_down, s, out).
  * scratch: at least more_moe_layer_scratch_bytes(N, h, s, M, k) bytes, 16-byte aligned, one for each call that may
  * overlap.  Asynchronous on `stream`; allocates nothing; may be captured into a graph.  The few-token kernel is a

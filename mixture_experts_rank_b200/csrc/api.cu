@@ -509,7 +509,9 @@ namespace {
 // dispatch and the grouped products.
 struct LayerBuffers {
   int32_t *idx, *counts, *offsets, *slots;
-  float *gate, *mid, *x_scale, *z, *logits;
+  float *gate, *mid, *mid_scale, *x_scale, *z, *logits;
+  __nv_bfloat16* mid_pair;
+  int8_t* mid_q;
   int8_t* Xq;
   unsigned int* barrier;
   void *dispatch, *experts;
@@ -526,8 +528,12 @@ LayerBuffers carve_layer(void* scratch, int64_t N, int h, int s, int M, int k, b
     b.barrier = c.take<unsigned int>(1);
     b.z = c.take<float>(N * 128);  // r <= 128
     b.logits = c.take<float>(N * M);
-    b.mid = c.take<float>(S * s);
-    if (int8) {
+    if (!int8) {
+      b.mid_pair = c.take<__nv_bfloat16>(2 * S * s);
+    } else {
+      b.mid = c.take<float>(S * s);
+      b.mid_q = c.take<int8_t>(S * s);
+      b.mid_scale = c.take<float>(S);
       b.Xq = c.take<int8_t>(N * h);
       b.x_scale = c.take<float>(N);
     }
@@ -582,7 +588,10 @@ more_status moe_layer(const void* X, const void* R1, const void* R2, const void*
   f.logits = b.logits;
   f.idx = b.idx;
   f.gate = b.gate;
+  f.mid_pair = b.mid_pair;
   f.mid = b.mid;
+  f.mid_q = b.mid_q;
+  f.mid_scale = b.mid_scale;
   f.barrier = b.barrier;
   f.out = out;
   f.N = N;

@@ -127,7 +127,10 @@ struct FewArgs {
   float *z, *logits;  // [N][r], [N][M]
   int32_t* idx;       // [N k]
   float* gate;        // [N k]
-  float* mid;         // [N k][s]
+  __nv_bfloat16* mid_pair;  // [2][N k][s]
+  float* mid;               // int8: [N k][s]
+  int8_t* mid_q;            // int8: [N k][s]
+  float* mid_scale;         // int8: [N k]
   unsigned int* barrier;
   void* out;
   int64_t N;

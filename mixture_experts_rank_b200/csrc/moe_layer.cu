@@ -1,21 +1,29 @@
 // The whole layer for a few tokens, in one cooperative kernel.
 //
 // The time of such a call is the latency of its steps and the reading of the selected experts' weights, once each, so
-// everything is laid out for those: no tensor cores (a handful of rows an expert), every step spread over all CTAs with
-// a barrier over the grid behind it, every warp streaming whole rows of weights.
+// every step is spread over all CTAs with a barrier over the grid behind it:
 //   1. z = x R1: a CTA takes 16 columns of a token's z, its warps parts of h.  With 8-bit weights other CTAs round x.
 //   2. The logits z R2: a warp takes 8 experts of a token, a lane one row of R2 (or r / 32 of them); the N x M logits of
 //      these few tokens go through scratch.
 //   3. A CTA takes a token's largest k logits and their softmax (for up to kSolo tokens every CTA does so itself, which
 //      saves a barrier).  Then every CTA groups the N k selections by expert, up to 8 a group: its own copy.
-//   4. Up: a warp takes row i of A_e and of B_e and the group's tokens; m = silu(a) * b goes to scratch in fp32.
-//      Where there are too few rows for the machine's warps, 2 to 8 warps share a row, each a part of h.
+//   4. Up: a warp takes 8 rows of A_e and the same 8 of B_e for a group's tokens; m = silu(a) * b goes to scratch.
+//      Where there are too few rows for the machine's warps, 2 to 16 warps of a CTA share them, each a part of h.
 //   5. Down: every CTA owns h / CTAs output channels for all experts, so a token's k contributions meet in its
 //      shared memory, and out[n] = sum_j gate * y is summed there in the order of j: no second pass over a row buffer,
 //      and no atomics on the result.
-// z is carried as the bf16 pair of the routing kernels; all else stays in fp32 until the output.  With 8-bit weights
-// the products are integer dot products (four an instruction); m is rounded to 8 bits when it is read, with its row's
-// largest magnitude found after the barrier.
+//
+// The products of 4 and 5 are warp MMAs (m16n8k16; k32 for 8 bits) with the weights as the 16 rows of A and a group's
+// up to 8 tokens as the columns of B.  The tensor cores are not what a few rows an expert need; their operand layout is:
+// one instruction takes 512 bytes of weights, where a thread's own multiply-adds, with their conversions and the
+// reductions over lanes, took longer than the reading (N = 64, h = 2048, s = 64: 2.6 TB/s in step 5).  A product's terms may
+// come in any order as long as both operands keep to it, so a lane's 16 contiguous bytes of a row serve as its fragments of two
+// MMAs without any shuffling.  Weights pass through a ring of asynchronous copies of each warp's own, 7 KB a warp in
+// flight, that runs on from one group to the next.
+//
+// z is carried as the bf16 pair of the routing kernels, and m as such a pair (about 16 bits), since B is bf16: two MMAs
+// where one would round m to 8 bits.  All sums are fp32.  With 8-bit weights sums are whole numbers and m is rounded to
+// 8 bits, its row's largest magnitude found after one more barrier.
 #include <algorithm>
 #include <atomic>
 
@@ -28,10 +36,15 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
-constexpr int kGroup = 8;  // selections of one expert that share a reading of its weights
+constexpr int kGroup = 8;  // selections of one expert that share a reading of its weights: the columns of an MMA
+constexpr int kRows = 16;  // rows of an MMA
 constexpr int64_t kFewTokens = 64;
-constexpr uint32_t kSmemMost = 200 * 1024;
-constexpr int kRowBlocks = 4;  // rows (times 32 / lanes a row) that a warp carries in the second product
+constexpr int kSolo = 2;         // tokens that every CTA routes for itself
+constexpr int kStages = 8;       // steps of a warp's ring
+constexpr uint32_t kEntry = 1024;  // a step: 16 rows x 64 bytes, two 16-byte pieces a lane
+constexpr uint32_t kRing = kWarps * kStages * kEntry;
+constexpr uint32_t kSmemMost = 200 * 1024;  // dynamic
+constexpr int kCandidates = 256;
 
 struct LayerArgs {
   const __nv_bfloat16 *X, *R1, *R2;
@@ -43,94 +56,74 @@ struct LayerArgs {
   float* logits;  // [N][M]
   int32_t* idx;   // [S]
   float* gate;    // [S]
-  float* mid;     // [S][s]
+  __nv_bfloat16 *mid_hi, *mid_lo;  // [S][s], m as a bf16 pair
+  float* mid;                      // int8: [S][s], and its 8 bits with their scales
+  int8_t* mid_q;
+  float* mid_scale;
   __nv_bfloat16* out;
   unsigned int* barrier;  // 0 at the start
   unsigned int* status;
   int N, h, r, s, M, k, S;
 };
 
-// ---- shared memory: the groups, the selections' output channels ------------------------------------------------
+// ---- shared memory ---------------------------------------------------------------------------------------------
 struct Shared {
+  uint32_t ring;       // shared address of the warps' rings
+  uint8_t* work;       // the ring's bytes, for steps that have no copies in flight
   int32_t* expert;     // [S] expert of a selection (-1: none)
-  int16_t* member;     // [S][kGroup] selections of a group
-  int16_t* lead;       // [S] group of a leading selection
+  float* gate;         // [S]
   int32_t* group_e;    // [S] expert of a group
   int32_t* group_n;    // [S] its selections
-  float* gate;         // [S]
-  float* top;          // [S] largest |m| (int8)
+  int16_t* member;     // [S][kGroup] selections of a group
   float* y;            // [S][R]
 };
 
 __host__ __device__ inline uint32_t round16(uint32_t v) { return (v + 15) & ~15u; }
 
 __host__ __device__ inline uint32_t layer_smem(int S, int R) {
-  return round16(4 * S) * 5 + round16(2 * kGroup * S) + round16(2 * S) + round16(4 * S * R) + 16;
+  return kRing + round16(4 * S) * 4 + round16(2 * kGroup * S) + round16(4 * S * R);
 }
 
-__device__ __forceinline__ Shared shared_at(uint8_t* p, int S, int R) {
+__device__ __forceinline__ Shared shared_at(uint8_t* p, int S) {
   Shared r;
+  r.ring = sm100::smem_u32(p);
+  r.work = p;
+  p += kRing;
   r.expert = reinterpret_cast<int32_t*>(p);
+  p += round16(4 * S);
+  r.gate = reinterpret_cast<float*>(p);
   p += round16(4 * S);
   r.group_e = reinterpret_cast<int32_t*>(p);
   p += round16(4 * S);
   r.group_n = reinterpret_cast<int32_t*>(p);
   p += round16(4 * S);
-  r.gate = reinterpret_cast<float*>(p);
-  p += round16(4 * S);
-  r.top = reinterpret_cast<float*>(p);
-  p += round16(4 * S);
   r.member = reinterpret_cast<int16_t*>(p);
   p += round16(2 * kGroup * S);
-  r.lead = reinterpret_cast<int16_t*>(p);
-  p += round16(2 * S);
   r.y = reinterpret_cast<float*>(p);
   return r;
 }
 
-// Weights are read once: they pass by L1.
-__device__ __forceinline__ uint4 load_weights(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
+// ---- small pieces -----------------------------------------------------------------------------------------------
 // bf16 pairs as fp32
-__device__ __forceinline__ void widen(uint32_t u, float& lo, float& hi) {
-  lo = __uint_as_float(u << 16);
-  hi = __uint_as_float(u & 0xffff0000u);
-}
-
 __device__ __forceinline__ void widen8(uint4 v, float (&x)[8]) {
-  widen(v.x, x[0], x[1]);
-  widen(v.y, x[2], x[3]);
-  widen(v.z, x[4], x[5]);
-  widen(v.w, x[6], x[7]);
-}
-
-__device__ __forceinline__ void dot8(float& acc, uint4 w, const float* x) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float lo, hi;
-    widen(u[i], lo, hi);
-    acc = fmaf(lo, x[2 * i], acc);
-    acc = fmaf(hi, x[2 * i + 1], acc);
+    x[2 * i] = __uint_as_float(u[i] << 16);
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
   }
 }
 
 // Sums V values over the warp; lane l ends with value l >> (5 - log2 V).
-template <int V, class T>
-__device__ __forceinline__ T reduce_scatter(T (&v)[V], int lane) {
+template <int V>
+__device__ __forceinline__ float reduce_scatter(float (&v)[V], int lane) {
   int d = 16;
 #pragma unroll
   for (int n = V; n > 1; n >>= 1, d >>= 1) {
     const bool up = lane & d;
 #pragma unroll
     for (int q = 0; q < n / 2; ++q) {
-      const T send = up ? v[q] : v[q + n / 2];
+      const float send = up ? v[q] : v[q + n / 2];
       v[q] = (up ? v[q + n / 2] : v[q]) + __shfl_xor_sync(0xffffffffu, send, d);
     }
   }
@@ -139,17 +132,18 @@ __device__ __forceinline__ T reduce_scatter(T (&v)[V], int lane) {
   return v[0];
 }
 
-template <int V>
-constexpr int log2_of() {
-  return V == 1 ? 0 : 1 + log2_of<(V > 1 ? V / 2 : 1)>();
+// Floats as keys of the same order.
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);  // -0 as 0
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Barrier number `turn` (from 1) over a cooperative grid; false once the wait has run out.
+// Barrier number `turn` (from 1) over a cooperative grid; false once the wait has run out.  One release and acquire of
+// one thread, which the CTA's own barriers extend to the others.
 __device__ bool grid_barrier(unsigned int* counter, unsigned turn, unsigned int* status, int* failed) {
   __syncthreads();
   if (threadIdx.x == 0) {
-    __threadfence();
-    atomicAdd(counter, 1u);
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(counter) : "memory");
     *failed = 0;
     const long long t0 = clock64();
     for (unsigned spin = 0;; ++spin) {
@@ -162,14 +156,14 @@ __device__ bool grid_barrier(unsigned int* counter, unsigned turn, unsigned int*
         break;
       }
     }
-    __threadfence();
   }
   __syncthreads();
   return *failed == 0;
 }
 
+// ---- routing ------------------------------------------------------------------------------------------------------
 // Step 1.  `part`: 16 sums a warp.
-__device__ void project_tokens(const LayerArgs& a, float (*part)[2 * kGroup]) {
+__device__ void project_tokens(const LayerArgs& a, float (*part)[16]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, blocks = a.r / 16;
   for (int u = blockIdx.x; u < a.N * blocks; u += gridDim.x) {
     const int n = u / blocks, b = (u - n * blocks) * 16;
@@ -179,18 +173,28 @@ __device__ void project_tokens(const LayerArgs& a, float (*part)[2 * kGroup]) {
     if ((lane & 1) == 0) part[warp][i - b] = v;
     __syncthreads();
     if (threadIdx.x < 16) {
-      float z = 0.f;
+      float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) z += part[w][threadIdx.x];
-      a.z[n * a.r + b + threadIdx.x] = split_bf16_pair(z);
+      for (int w = 0; w < kWarps; ++w) sum += part[w][threadIdx.x];
+      a.z[n * a.r + b + threadIdx.x] = split_bf16_pair(sum);
     }
     __syncthreads();
   }
 }
 
+// The largest of a CTA's values.
+__device__ __forceinline__ float block_max(float v, float* warp_tops) {
+  // the float order of magnitudes is their bits' order
+  v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+  if ((threadIdx.x & 31) == 0) warp_tops[threadIdx.x >> 5] = v;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) v = fmaxf(v, warp_tops[w]);
+  return v;
+}
+
 // x in 8 bits, a token a CTA, from the last CTA down (the first have z to compute).
 __device__ void round_tokens(const LayerArgs& a, float* warp_tops) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int n = gridDim.x - 1 - blockIdx.x; n < a.N; n += gridDim.x) {
     const uint4* src = reinterpret_cast<const uint4*>(a.X + (size_t)n * a.h);
     float top = 0.f, x[8];
@@ -199,12 +203,7 @@ __device__ void round_tokens(const LayerArgs& a, float* warp_tops) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
     }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if (lane == 0) warp_tops[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, warp_tops[w]);
+    top = block_max(top, warp_tops);
     const float div = top > 0.f ? top : 1.f, inv = __fdiv_rn(127.f, div);
     for (int c = threadIdx.x; c < a.h / 8; c += kThreads) {
       widen8(src[c], x);
@@ -225,74 +224,173 @@ __device__ void expert_logits(const LayerArgs& a) {
   for (int u = warp; u < mine * a.N; u += kWarps) {
     const int j = u / a.N, n = u - j * a.N;
     const int e0 = 8 * ((int)blockIdx.x + (int)gridDim.x * j);
-    uint4 w[4];
-    float zi[4], acc[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = lane + 32 * i;
-      const bool in = row < a.r;
-      w[i] = in ? __ldg(reinterpret_cast<const uint4*>(a.R2 + (size_t)row * a.M + e0)) : make_uint4(0, 0, 0, 0);
-      zi[i] = in ? a.z[n * a.r + row] : 0.f;
-    }
+    float acc[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) acc[q] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int row = lane; row < a.r; row += 32) {
       float x[8];
-      widen8(w[i], x);
+      widen8(__ldg(reinterpret_cast<const uint4*>(a.R2 + (size_t)row * a.M + e0)), x);
+      const float zi = a.z[n * a.r + row];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) acc[q] = fmaf(zi[i], x[q], acc[q]);
+      for (int q = 0; q < 8; ++q) acc[q] = fmaf(zi, x[q], acc[q]);
     }
+    __syncwarp();
     const float v = reduce_scatter<8>(acc, lane);
     if ((lane & 3) == 0) a.logits[(size_t)n * a.M + e0 + (lane >> 2)] = v;
   }
 }
 
 // Step 3 for token n: its selections and gates at idx and gate (shared or global memory).
-template <int KCAP>
-__device__ void select_experts(const LayerArgs& a, int n, float (*pv)[KCAP], int (*pe)[KCAP], int32_t* idx,
-                               float* gate) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+//   Every thread's largest key is known at once; the k-th largest of those bounds the k-th largest logit from below.
+//   Twelve bits of that bound, a vote each, leave a handful of candidates, which rank one another in parallel: rounds of
+//   a block-wide largest value cost 200 cycles each, 16 of them for k = 8.  More candidates than kCandidates (logits that are
+//   all but equal) are thinned by the bound's other bits, and equal ones by their experts.
+struct Select {
+  uint32_t key[kCandidates];
+  int expert[kCandidates];
+  float value[MORE_KMAX];
+  int count;
+};
+
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+__device__ void select_experts(const LayerArgs& a, int n, Select& s, int32_t* idx, float* gate) {
   const float* l = a.logits + (size_t)n * a.M;
-  TopList<KCAP> list;
-  list.init();
-  for (int e = threadIdx.x; e < a.M; e += 4 * kThreads) {
-    float v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = e + i * kThreads < a.M ? l[e + i * kThreads] : -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) list.insert(v[i], e + i * kThreads);
+  uint32_t top = 0;  // below every number's key; a NaN logit is never chosen
+  for (int e = threadIdx.x; e < a.M; e += kThreads) {
+    const float v = l[e];
+    if (v == v) top = max(top, key_of(v));
   }
-  float v;
-  int e;
-  warp_merge_topk<KCAP>(list, a.k, lane, v, e);
-  if (lane < KCAP) {
-    pv[warp][lane] = v;
-    pe[warp][lane] = e;
+  uint32_t bound = 0;
+  int bit = 31;
+  int limit = 0x7fffffff;  // candidates at the bound itself: only experts below this
+  auto collect = [&]() {
+    __syncthreads();
+    if (threadIdx.x == 0) s.count = 0;
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.M; e += kThreads) {
+      const float v = l[e];
+      const uint32_t key = key_of(v);
+      if (v == v && key >= bound && (key > bound || e < limit)) {
+        const int at = atomicAdd(&s.count, 1);
+        if (at < kCandidates) {
+          s.key[at] = key;
+          s.expert[at] = e;
+        }
+      }
+    }
+    __syncthreads();
+    return s.count;
+  };
+  auto refine = [&](int last) {
+    for (; bit >= last; --bit) {
+      const uint32_t trial = bound | 1u << bit;
+      if (__syncthreads_count(top >= trial) >= a.k) bound = trial;
+    }
+  };
+  refine(20);
+  int count = collect();
+  if (count > kCandidates) {
+    refine(0);
+    count = collect();
+    if (count > kCandidates) {
+      // The bound is some thread's largest key, reached by at least k of them, so fewer than k threads hold a larger
+      // key, but those may hold many, and so may the ties.  First the larger keys alone, if they suffice, else the
+      // lowest experts of the ties beside them: both by bisection.
+      uint32_t lo = bound, hi = 0xffffffffu;  // at least k keys >= lo; find the largest such lo
+      while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo) / 2 + 1;
+        int c = 0;
+        for (int e = threadIdx.x; e < a.M; e += kThreads) {
+          const float v = l[e];
+          c += v == v && key_of(v) >= mid;
+        }
+        // a thread counts as many as it has, up to k
+        int total = 0;
+        for (int j = 0; j < a.k; ++j) total += __syncthreads_count(c > j);
+        if (total >= a.k)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      bound = lo;  // the k-th largest key itself: fewer than k are larger
+      int from = 0, to = a.M;  // the first experts [0, to) hold k keys at or above it
+      while (from < to) {
+        const int half = (from + to) / 2;
+        int c = 0;
+        for (int e = threadIdx.x; e < a.M; e += kThreads) {
+          const float v = l[e];
+          const uint32_t key = key_of(v);
+          c += v == v && (key > bound || (key == bound && e < half));
+        }
+        int total = 0;
+        for (int j = 0; j < a.k; ++j) total += __syncthreads_count(c > j);
+        if (total >= a.k)
+          to = half;
+        else
+          from = half + 1;
+      }
+      limit = to;
+      count = collect();
+    }
+  }
+  // ranks
+  for (int c = threadIdx.x; c < count; c += kThreads) {
+    const uint32_t key = s.key[c];
+    const int e = s.expert[c];
+    int rank = 0;
+    for (int o = 0; o < count; ++o) rank += s.key[o] > key || (s.key[o] == key && s.expert[o] < e);
+    if (rank < a.k) {
+      s.value[rank] = value_of(key);
+      idx[n * a.k + rank] = e;
+    }
   }
   __syncthreads();
-  if (warp == 0) {
-    TopList<KCAP> all;
-    all.init();
-    for (int q = lane; q < kWarps * KCAP; q += 32)
-      if (q % KCAP < a.k) all.insert_any(pv[q / KCAP][q % KCAP], pe[q / KCAP][q % KCAP]);
-    warp_merge_topk<KCAP>(all, a.k, lane, v, e);
-    const float top = __shfl_sync(0xffffffffu, v, 0);
-    const float ex = lane < a.k ? expf(v - top) : 0.f;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    const bool in = lane < a.k && lane < count;
+    const float top_v = s.value[0];
+    const float ex = in ? expf(s.value[lane] - top_v) : 0.f;
     float sum = ex;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d, 16);
     if (lane < a.k) {
-      idx[n * a.k + lane] = e;
-      gate[n * a.k + lane] = ex / sum;
+      gate[n * a.k + lane] = in ? ex / sum : 0.f;
+      if (!in) idx[n * a.k + lane] = -1;  // fewer than k numbers among the logits
     }
   }
   __syncthreads();
 }
 
-// Groups the selections by expert, in their order; the number of groups.
-__device__ int group_selections(const LayerArgs& a, const Shared& sh, bool solo, int* counts) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Groups the selections by expert, up to kGroup a group, the same way in every CTA; the number of groups.  A hash table
+// in the ring's space holds each expert's selections so far and the lowest of them; experts are numbered in the order
+// of those, groups of one expert follow one another.  Up to kGroup selections of an expert take the columns of its one
+// group as they come: a selection's sums are the same in every column.
+constexpr int kTable = 2048;
+
+__device__ __forceinline__ int place_of(int32_t* keys, int key) {
+  int at = (int)(((uint32_t)key * 2654435761u) >> 21);  // 11 bits
+  for (int tries = 0; tries < kTable; ++tries) {
+    const int old = atomicCAS(&keys[at], -1, key);
+    if (old == -1 || old == key) return at;
+    at = (at + 1) & (kTable - 1);
+  }
+  return 0;  // not reached: at most 1024 keys
+}
+
+__device__ int group_selections(const LayerArgs& a, const Shared& sh, bool solo, int* warp_sums) {
+  int32_t* t_expert = reinterpret_cast<int32_t*>(sh.work);
+  int32_t* t_count = t_expert + kTable;
+  int32_t* t_first = t_count + kTable;
+  int32_t* t_base = t_first + kTable;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < kTable; i += kThreads) {
+    t_expert[i] = -1;
+    t_count[i] = 0;
+    t_first[i] = 0x7fffffff;
+  }
   for (int i = threadIdx.x; i < a.S; i += kThreads) {
     const int e = solo ? sh.expert[i] : a.idx[i];
     if (!solo) sh.gate[i] = a.gate[i];
@@ -301,372 +399,409 @@ __device__ int group_selections(const LayerArgs& a, const Shared& sh, bool solo,
     sh.expert[i] = ok ? e : -1;
   }
   __syncthreads();
+  int at[2] = {-1, -1}, nth[2] = {0, 0};  // S <= 2 kThreads
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int i = threadIdx.x + q * kThreads, e = i < a.S ? sh.expert[i] : -1;
+    if (e < 0) continue;
+    at[q] = place_of(t_expert, e);
+    nth[q] = atomicAdd(&t_count[at[q]], 1);
+    atomicMin(&t_first[at[q]], i);
+  }
+  __syncthreads();
   int groups = 0;
-  for (int base = 0; base < a.S; base += kThreads) {
-    const int i = base + threadIdx.x;
-    const int e = i < a.S ? sh.expert[i] : -1;
-    int before = 0, lead = i;  // earlier selections of the same expert; the one that leads this one's group
-    if (e >= 0) {
-      for (int q = 0; q < i; ++q)
-        if (sh.expert[q] == e) {
-          if (before % kGroup == 0) lead = q;
-          ++before;
-        }
-      if (before % kGroup == 0) lead = i;
+#pragma unroll 1
+  for (int q = 0; q < 2 && q * kThreads < a.S; ++q) {
+    const int i = threadIdx.x + q * kThreads;
+    const bool leads = at[q] >= 0 && t_first[at[q]] == i;
+    const int mine = leads ? (t_count[at[q]] + kGroup - 1) / kGroup : 0;
+    int sum = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += o;
     }
-    const bool leads = e >= 0 && lead == i;
-    const unsigned vote = __ballot_sync(0xffffffffu, leads);
-    if (lane == 0) counts[warp] = __popc(vote);
+    if (lane == 31) warp_sums[warp] = sum;
     __syncthreads();
-    int at = groups;
+    int base = groups;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      at += w < warp ? counts[w] : 0;
-      groups += counts[w];
+      const int o = warp_sums[w];
+      base += w < warp ? o : 0;
+      groups += o;
     }
-    if (leads) {
-      const int g = at + __popc(vote & ((1u << lane) - 1));
-      sh.lead[i] = (int16_t)g;
-      sh.group_e[g] = e;
-      sh.group_n[g] = 0;
-    }
-    __syncthreads();
-    if (e >= 0) {
-      const int g = sh.lead[lead];
-      sh.member[g * kGroup + before % kGroup] = (int16_t)i;
-      atomicAdd(&sh.group_n[g], 1);
-    }
+    if (leads) t_base[at[q]] = base + sum - mine;
     __syncthreads();
   }
+#pragma unroll 1
+  for (int q = 0; q < 2; ++q) {
+    if (at[q] < 0) continue;
+    const int i = threadIdx.x + q * kThreads, count = t_count[at[q]];
+    if (count > kGroup) {  // which group a selection is in has to be the same everywhere
+      nth[q] = 0;
+      for (int o = 0; o < i; ++o) nth[q] += sh.expert[o] == sh.expert[i];
+    }
+    const int g = t_base[at[q]] + nth[q] / kGroup;
+    sh.member[g * kGroup + nth[q] % kGroup] = (int16_t)i;
+    if (nth[q] % kGroup == 0) {
+      sh.group_e[g] = sh.expert[i];
+      sh.group_n[g] = min(kGroup, count - nth[q]);
+    }
+  }
+  __syncthreads();
   return groups;
 }
 
-// Partial a and b of up to TB selections for this warp's part of h; lane l gets value l >> (5 - log2(2 TB)) of
-// (a_0, b_0, a_1, b_1, ...).
-template <int TB>
-__device__ __forceinline__ float up_bf16(const LayerArgs& a, const uint8_t* ra, const uint8_t* rb, const int (&tok)[TB],
-                                         int part, int parts, int lane) {
-  float acc[2 * TB];
-#pragma unroll
-  for (int i = 0; i < 2 * TB; ++i) acc[i] = 0.f;
-  constexpr int kAhead = 4;
-  const int step = 256 * parts;
-  for (int c = part * 256 + lane * 8; c < a.h; c += kAhead * step) {
-    uint4 wa[kAhead], wb[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int col = c + i * step;
-      if (col < a.h) {
-        wa[i] = load_weights(ra + 2 * (size_t)col);
-        wb[i] = load_weights(rb + 2 * (size_t)col);
-      } else {
-        wa[i] = wb[i] = make_uint4(0, 0, 0, 0);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int col = c + i * step;
-      if (col >= a.h) break;
-#pragma unroll
-      for (int t = 0; t < TB; ++t) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.X + (size_t)tok[t] * a.h + col));
-        float x[8];
-        widen8(v, x);
-        dot8(acc[2 * t], wa[i], x);
-        dot8(acc[2 * t + 1], wb[i], x);
-      }
-    }
-  }
-  return reduce_scatter<2 * TB>(acc, lane);
+// ---- products -----------------------------------------------------------------------------------------------------
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// With kStages - 1 steps in flight: waits for the oldest.
+__device__ __forceinline__ void wait_oldest() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
 }
 
-__device__ __forceinline__ int dot16(uint4 w, uint4 x, int acc) {
-  acc = __dp4a((int)w.x, (int)x.x, acc);
-  acc = __dp4a((int)w.y, (int)x.y, acc);
-  acc = __dp4a((int)w.z, (int)x.z, acc);
-  return __dp4a((int)w.w, (int)x.w, acc);
+template <bool I8>
+struct Sums {
+  float v[4];
+};
+template <>
+struct Sums<true> {
+  int v[4];
+};
+
+__device__ __forceinline__ void mma(Sums<false>& c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c.v[0]), "+f"(c.v[1]), "+f"(c.v[2]), "+f"(c.v[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma(Sums<true>& c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+r"(c.v[0]), "+r"(c.v[1]), "+r"(c.v[2]), "+r"(c.v[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int TB>
-__device__ __forceinline__ float up_int8(const LayerArgs& a, const uint8_t* ra, const uint8_t* rb, const int (&tok)[TB],
-                                         int part, int parts, int lane) {
-  int acc[2 * TB];
-#pragma unroll
-  for (int i = 0; i < 2 * TB; ++i) acc[i] = 0;
-  constexpr int kAhead = 4;
-  const int step = 512 * parts;
-  for (int c = part * 512 + lane * 16; c < a.h; c += kAhead * step) {
-    uint4 wa[kAhead], wb[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int col = c + i * step;
-      if (col < a.h) {
-        wa[i] = load_weights(ra + (size_t)col);
-        wb[i] = load_weights(rb + (size_t)col);
-      } else {
-        wa[i] = wb[i] = make_uint4(0, 0, 0, 0);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int col = c + i * step;
-      if (col >= a.h) break;
-#pragma unroll
-      for (int t = 0; t < TB; ++t) {
-        const uint4 x = *reinterpret_cast<const uint4*>(a.Xq + (size_t)tok[t] * a.h + col);  // written by this kernel
-        acc[2 * t] = dot16(wa[i], x, acc[2 * t]);
-        acc[2 * t + 1] = dot16(wb[i], x, acc[2 * t + 1]);
-      }
-    }
-  }
-  // whole sums of 8-bit products stay below 2^24 for h <= 1024 only: they are added in 32-bit integers
-  return __int_as_float(reduce_scatter<2 * TB>(acc, lane));
+// 64 bytes of K: rows lane / 4 and lane / 4 + 8 of the weights, column lane / 4 of the other operand, bytes
+// 16 (lane % 4) on of each.
+template <bool I8>
+__device__ __forceinline__ void step_products(Sums<I8>& c, uint4 w0, uint4 w1, uint4 x) {
+  mma(c, w0.x, w1.x, w0.y, w1.y, x.x, x.y);
+  mma(c, w0.z, w1.z, w0.w, w1.w, x.z, x.w);
 }
+
+// A warp's ring: steps are fetched kStages - 1 ahead, in the order that `Next` gives them.
+struct RingAt {
+  uint32_t base;  // of this lane's pieces
+  int in = 0, out = 0;
+  __device__ __forceinline__ uint32_t fill() {
+    const uint32_t at = base + in * kEntry;
+    in = (in + 1) & (kStages - 1);
+    return at;
+  }
+  __device__ __forceinline__ uint32_t drain() {
+    const uint32_t at = base + out * kEntry;
+    out = (out + 1) & (kStages - 1);
+    return at;
+  }
+};
 
 __device__ __forceinline__ float silu_times(float a, float b) { return a * __fdividef(1.f, 1.f + expf(-a)) * b; }
 
-template <bool I8, int TB>
-__device__ __forceinline__ float up_unit(const LayerArgs& a, const Shared& sh, int g, int i, int n, int part, int parts,
-                                         int lane) {
-  int tok[TB];
+// m of rows i of group g's selections 2 (lane % 4) and the next, from a (sums 0 and 1) and b (2 and 3).
+template <bool I8>
+__device__ __forceinline__ void finish_up(const LayerArgs& a, const Shared& sh, int g, int i, int lane,
+                                          const Sums<I8>& c) {
+  const int n = sh.group_n[g];
 #pragma unroll
-  for (int t = 0; t < TB; ++t) tok[t] = sh.member[g * kGroup + min(t, n - 1)] / a.k;
-  const size_t row = ((size_t)sh.group_e[g] * 2 * a.s + i) * a.h, to_b = (size_t)a.s * a.h;
-  const uint8_t* w = static_cast<const uint8_t*>(a.W_up);
-  if constexpr (I8) return up_int8<TB>(a, w + row, w + row + to_b, tok, part, parts, lane);
-  return up_bf16<TB>(a, w + 2 * row, w + 2 * (row + to_b), tok, part, parts, lane);
+  for (int q = 0; q < 2; ++q) {
+    const int col = 2 * (lane & 3) + q;
+    if (col >= n) continue;
+    const int slot = sh.member[g * kGroup + col];
+    float va, vb;
+    if constexpr (I8) {
+      const float* sc = a.up_scale + (size_t)sh.group_e[g] * 2 * a.s + i;
+      const float xs = a.x_scale[slot / a.k];
+      va = (float)c.v[q] * (xs * sc[0]);
+      vb = (float)c.v[q + 2] * (xs * sc[a.s]);
+    } else {
+      va = c.v[q];
+      vb = c.v[q + 2];
+    }
+    const float m = silu_times(va, vb);
+    const size_t at = (size_t)slot * a.s + i;
+    if constexpr (I8) {
+      a.mid[at] = m;
+    } else {
+      const __nv_bfloat16 hi = __float2bfloat16_rn(m);
+      a.mid_hi[at] = hi;
+      a.mid_lo[at] = __float2bfloat16_rn(m - __bfloat162float(hi));
+    }
+  }
 }
 
-// a and b of selection q of group g for row i: m to scratch.
+// Step 4.  Unit u: rows 8 (u % (s / 8)) on of group u / (s / 8).  `parts` warps a unit, each a run of its steps.
 template <bool I8>
-__device__ __forceinline__ void finish_up(const LayerArgs& a, const Shared& sh, int g, int i, int q, float va, float vb) {
-  const int slot = sh.member[g * kGroup + q];
-  if constexpr (I8) {
-    const float* sc = a.up_scale + (size_t)sh.group_e[g] * 2 * a.s + i;
-    const float xs = a.x_scale[slot / a.k];
-    va = (float)__float_as_int(va) * (xs * sc[0]);
-    vb = (float)__float_as_int(vb) * (xs * sc[a.s]);
-  }
-  a.mid[(size_t)slot * a.s + i] = silu_times(va, vb);
-}
-
-template <bool I8, int TB>
-__device__ __forceinline__ void up_whole(const LayerArgs& a, const Shared& sh, int g, int i, int n, int lane) {
-  const float v = up_unit<I8, TB>(a, sh, g, i, n, 0, 1, lane);
-  constexpr int sft = 5 - log2_of<2 * TB>();
-  const float o = __shfl_xor_sync(0xffffffffu, v, 1 << sft);
-  const int val = lane >> sft, q = val >> 1;
-  if ((val & 1) == 0 && (lane & ((1 << sft) - 1)) == 0 && q < n) finish_up<I8>(a, sh, g, i, q, v, o);
-}
-
-template <bool I8, int TB>
-__device__ __forceinline__ void up_part(const LayerArgs& a, const Shared& sh, int g, int i, int n, int part, int parts,
-                                        int lane, float* to) {
-  const float v = up_unit<I8, TB>(a, sh, g, i, n, part, parts, lane);
-  constexpr int sft = 5 - log2_of<2 * TB>();
-  if ((lane & ((1 << sft) - 1)) == 0) to[lane >> sft] = v;
-}
-
-#define MORE_BY_COUNT(n, CALL) \
-  if (n == 1) {                \
-    CALL(1);                   \
-  } else if (n == 2) {         \
-    CALL(2);                   \
-  } else if (n <= 4) {         \
-    CALL(4);                   \
-  } else {                     \
-    CALL(8);                   \
-  }
-
-template <bool I8>
-__device__ void up_phase(const LayerArgs& a, const Shared& sh, int groups, float (*part)[2 * kGroup]) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int units = groups * a.s;
-  const int each = (units + gridDim.x - 1) / gridDim.x;  // rows a CTA
-  // warps a row: enough rows for every warp of the machine, or the row in up to 8 parts
-  const int parts = each >= 12 ? 1 : each >= 6 ? 2 : each >= 3 ? 4 : 8;
-  if (parts == 1) {
-    for (int u = blockIdx.x + gridDim.x * warp; u < units; u += gridDim.x * kWarps) {
-      const int g = u / a.s, i = u - g * a.s, n = sh.group_n[g];
-#define MORE_CALL(TB) up_whole<I8, TB>(a, sh, g, i, n, lane)
-      MORE_BY_COUNT(n, MORE_CALL)
-#undef MORE_CALL
-    }
-    return;
-  }
-  const int per = kWarps / parts;  // rows of a CTA at a time
-  for (int j = 0; j < each; j += per) {
-    const int mine = j + warp / parts, u = blockIdx.x + gridDim.x * mine;
-    if (mine < each && u < units) {
-      const int g = u / a.s, i = u - g * a.s, n = sh.group_n[g];
-#define MORE_CALL(TB) up_part<I8, TB>(a, sh, g, i, n, warp % parts, parts, lane, part[warp])
-      MORE_BY_COUNT(n, MORE_CALL)
-#undef MORE_CALL
-    }
-    __syncthreads();
-    if (threadIdx.x < per * kGroup) {
-      const int r = threadIdx.x / kGroup, q = threadIdx.x % kGroup, ur = blockIdx.x + gridDim.x * (j + r);
-      if (j + r < each && ur < units) {
-        const int g = ur / a.s, i = ur - g * a.s;
-        if (q < sh.group_n[g]) {
-          float va = 0.f, vb = 0.f;
-          int ia = 0, ib = 0;
-          for (int w = r * parts; w < (r + 1) * parts; ++w) {
-            if constexpr (I8) {
-              ia += __float_as_int(part[w][2 * q]);
-              ib += __float_as_int(part[w][2 * q + 1]);
-            } else {
-              va += part[w][2 * q];
-              vb += part[w][2 * q + 1];
-            }
-          }
-          if constexpr (I8) {
-            va = __int_as_float(ia);
-            vb = __int_as_float(ib);
-          }
-          finish_up<I8>(a, sh, g, i, q, va, vb);
-        }
-      }
-    }
-    __syncthreads();
-  }
-}
-
-// Rows r0 + rb * rows + lane / L (rb < kRowBlocks) of expert e for up to TB selections of group g.
-template <bool I8, int TB>
-__device__ __forceinline__ void down_unit(const LayerArgs& a, const Shared& sh, int g, int n, int o0, int R, int r0,
-                                          int L, int lane) {
-  const int rows = 32 / L, sub = lane / L, l = lane % L;
-  const int e = sh.group_e[g];
+__device__ void up_phase(const LayerArgs& a, const Shared& sh, int groups, Sums<I8> (*red)[kWarps][32]) {
   constexpr int kBytes = I8 ? 1 : 2, kVec = 16 / kBytes;
-  const uint8_t* w = static_cast<const uint8_t*>(a.W_down) + ((size_t)e * a.h + o0) * a.s * kBytes;
-  float acc[TB][kRowBlocks];
-  int iacc[TB][kRowBlocks];
-#pragma unroll
-  for (int t = 0; t < TB; ++t)
-#pragma unroll
-    for (int b = 0; b < kRowBlocks; ++b) {
-      acc[t][b] = 0.f;
-      iacc[t][b] = 0;
-    }
-  int slot[TB];
-#pragma unroll
-  for (int t = 0; t < TB; ++t) slot[t] = sh.member[g * kGroup + min(t, n - 1)];
-  for (int c = l * kVec; c < a.s; c += L * kVec) {
-    uint4 v[kRowBlocks];
-#pragma unroll
-    for (int b = 0; b < kRowBlocks; ++b) {
-      const int r = r0 + b * rows + sub;
-      v[b] = r < R ? load_weights(w + ((size_t)r * a.s + c) * kBytes) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int t = 0; t < TB; ++t) {
-      const float4* m = reinterpret_cast<const float4*>(a.mid + (size_t)slot[t] * a.s + c);
-      if constexpr (I8) {
-        const float top = sh.top[slot[t]];
-        const float f = top > 0.f ? __fdiv_rn(127.f, top) : 0.f;
-        uint32_t q[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 x = m[i];
-          q[i] = (uint32_t)(__float2int_rn(x.x * f) & 255) | (uint32_t)(__float2int_rn(x.y * f) & 255) << 8 |
-                 (uint32_t)(__float2int_rn(x.z * f) & 255) << 16 | (uint32_t)(__float2int_rn(x.w * f) & 255) << 24;
-        }
-#pragma unroll
-        for (int b = 0; b < kRowBlocks; ++b) iacc[t][b] = dot16(v[b], make_uint4(q[0], q[1], q[2], q[3]), iacc[t][b]);
-      } else {
-        const float4 x0 = m[0], x1 = m[1];
-        const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-#pragma unroll
-        for (int b = 0; b < kRowBlocks; ++b) dot8(acc[t][b], v[b], x);
-      }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int eights = a.s / 8, units = groups * eights, steps = (a.h + 4 * kVec - 1) / (4 * kVec);
+  // The fewest steps a warp, a round's end counted as two more: rounds of all warps' units, shorter with more parts.
+  int parts = 1, best = 0x7fffffff;
+  for (int p = 1; p <= kWarps; p *= 2) {
+    const int per_round = (int)gridDim.x * (kWarps / p), rounds = (units + per_round - 1) / per_round;
+    const int cost = rounds * ((steps + p - 1) / p + (p > 1 ? 2 : 0));
+    if (cost < best) {
+      best = cost;
+      parts = p;
     }
   }
-#pragma unroll
-  for (int t = 0; t < TB; ++t) {
-    if (t >= n) break;
-#pragma unroll
-    for (int b = 0; b < kRowBlocks; ++b) {
-      const int r = r0 + b * rows + sub;
-      float y;
-      if constexpr (I8) {
-        for (int d = L / 2; d >= 1; d >>= 1) iacc[t][b] += __shfl_xor_sync(0xffffffffu, iacc[t][b], d);
-        const float sc = r < R ? a.down_scale[(size_t)e * a.h + o0 + r] : 0.f;
-        y = (float)iacc[t][b] * (__fdiv_rn(sh.top[slot[t]], 127.f) * sc);
-      } else {
-        for (int d = L / 2; d >= 1; d >>= 1) acc[t][b] += __shfl_xor_sync(0xffffffffu, acc[t][b], d);
-        y = acc[t][b];
+  const int each = kWarps / parts, stride = (int)gridDim.x * each;
+  const int first = (int)blockIdx.x * each, part = warp % parts;
+  const int s0 = steps * part / parts, s1 = steps * (part + 1) / parts;
+  const int piece = (lane & 3) * kVec;
+  const size_t to_b = (size_t)a.s * a.h * kBytes;
+  RingAt ring{sh.ring + warp * kStages * kEntry + lane * 16};
+  // what is fetched next
+  int fu = first + warp / parts, fs = s0;
+  const uint8_t* row = nullptr;
+  auto locate = [&]() {
+    if (fu >= units) return;
+    const int g = fu / eights, i = (fu - g * eights) * 8 + (lane >> 2);
+    row = static_cast<const uint8_t*>(a.W_up) + (((size_t)sh.group_e[g] * 2 * a.s + i) * a.h + piece) * kBytes;
+  };
+  locate();
+  auto fetch = [&]() {
+    const uint32_t at = ring.fill();
+    if (fu < units && s0 < s1) {
+      const int col = fs * 4 * kVec;
+      if (col + piece < a.h) {
+        copy16(at, row + (size_t)col * kBytes);
+        copy16(at + 512, row + to_b + (size_t)col * kBytes);
       }
-      if (l == 0 && r < R) sh.y[slot[t] * R + r] = y;
+      if (++fs == s1) {
+        fs = s0;
+        fu += stride;
+        locate();
+      }
+    }
+    commit_copies();
+  };
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) fetch();
+  int parity = 0;
+  for (int u0 = first; u0 < units; u0 += stride) {
+    const int u = u0 + warp / parts;
+    Sums<I8> c = {};
+    int g = 0, i = 0;
+    if (u < units) {
+      g = u / eights;
+      i = (u - g * eights) * 8 + (lane >> 2);
+      const int tok = sh.member[g * kGroup + min(lane >> 2, sh.group_n[g] - 1)] / a.k;
+      const uint8_t* x = (I8 ? reinterpret_cast<const uint8_t*>(a.Xq) : reinterpret_cast<const uint8_t*>(a.X)) +
+                         ((size_t)tok * a.h + piece) * kBytes;
+#pragma unroll 2
+      for (int st = s0; st < s1; ++st) {
+        const int col = st * 4 * kVec;
+        const bool in = col + piece < a.h;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        const uint4 xv = in ? *reinterpret_cast<const uint4*>(x + (size_t)col * kBytes) : zero;
+        wait_oldest();
+        const uint32_t at = ring.drain();
+        const uint4 w0 = in ? sm100::ld_shared_v4(at) : zero, w1 = in ? sm100::ld_shared_v4(at + 512) : zero;
+        fetch();
+        step_products<I8>(c, w0, w1, xv);
+      }
+    }
+    if (parts == 1) {
+      if (u < units) finish_up<I8>(a, sh, g, i, lane, c);
+    } else {
+      red[parity][warp][lane] = c;
+      __syncthreads();
+      const int ur = u0 + warp;  // warp w sums unit w of the round
+      if (warp < each && ur < units) {
+        Sums<I8> t = red[parity][warp * parts][lane];
+        for (int p = 1; p < parts; ++p)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) t.v[q] += red[parity][warp * parts + p][lane].v[q];
+        const int gr = ur / eights;
+        finish_up<I8>(a, sh, gr, (ur - gr * eights) * 8 + (lane >> 2), lane, t);
+      }
+      parity ^= 1;
     }
   }
 }
+
+// The middle rows in 8 bits: a selection a CTA.
+__device__ void round_middles(const LayerArgs& a, const Shared& sh, float* warp_tops) {
+  for (int i = blockIdx.x; i < a.S; i += gridDim.x) {
+    if (sh.expert[i] < 0) continue;
+    const float4* src = reinterpret_cast<const float4*>(a.mid + (size_t)i * a.s);
+    float top = 0.f;
+    for (int c = threadIdx.x; c < a.s / 4; c += kThreads) {
+      const float4 f = src[c];
+      top = fmaxf(fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f.z), fabsf(f.w)));
+    }
+    top = block_max(top, warp_tops);
+    const float div = top > 0.f ? top : 1.f, inv = __fdiv_rn(127.f, div);
+    for (int c = threadIdx.x; c < a.s / 4; c += kThreads) {
+      const float4 f = src[c];
+      char4 o;
+      o.x = round8(f.x, div, inv);
+      o.y = round8(f.y, div, inv);
+      o.z = round8(f.z, div, inv);
+      o.w = round8(f.w, div, inv);
+      reinterpret_cast<char4*>(a.mid_q + (size_t)i * a.s)[c] = o;
+    }
+    if (threadIdx.x == 0) a.mid_scale[i] = __fdiv_rn(top, 127.f);
+    __syncthreads();
+  }
+}
+
+// Step 5.  Unit u: rows 16 (u % tiles) on of this CTA's for group u / tiles.  The first steps' copies start before the
+// barrier: they need the groups alone.
+template <bool I8>
+struct Down {
+  static constexpr int kBytes = I8 ? 1 : 2, kVec = 16 / kBytes;
+  const LayerArgs& a;
+  const Shared& sh;
+  int o0, R, tiles, units, steps, piece, lane, warp;
+  RingAt ring;
+  int fu, fs;
+  const uint8_t* row;
+
+  __device__ Down(const LayerArgs& a_, const Shared& sh_, int groups, int rows_each) : a(a_), sh(sh_) {
+    warp = threadIdx.x >> 5;
+    lane = threadIdx.x & 31;
+    o0 = blockIdx.x * rows_each;
+    R = min(rows_each, a.h - o0);
+    tiles = R > 0 ? (R + kRows - 1) / kRows : 0;
+    units = groups * tiles;
+    steps = (a.s + 4 * kVec - 1) / (4 * kVec);
+    piece = (lane & 3) * kVec;
+    ring.base = sh.ring + warp * kStages * kEntry + lane * 16;
+    fu = warp;
+    fs = 0;
+    locate();
+  }
+  __device__ __forceinline__ void locate() {
+    if (fu >= units) return;
+    const int g = fu / tiles, r = (fu - g * tiles) * kRows + (lane >> 2);
+    row = static_cast<const uint8_t*>(a.W_down) + (((size_t)sh.group_e[g] * a.h + o0 + r) * a.s + piece) * kBytes;
+  }
+  __device__ __forceinline__ void fetch() {
+    const uint32_t at = ring.fill();
+    if (fu < units) {
+      const int col = fs * 4 * kVec, r = fu % tiles * kRows + (lane >> 2);
+      if (col + piece < a.s) {
+        if (r < R) copy16(at, row + (size_t)col * kBytes);
+        if (r + 8 < R) copy16(at + 512, row + ((size_t)8 * a.s + col) * kBytes);
+      }
+      if (++fs == steps) {
+        fs = 0;
+        fu += kWarps;
+        locate();
+      }
+    }
+    commit_copies();
+  }
+  __device__ void start() {
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) fetch();
+    for (int i = threadIdx.x; i < a.S * max(R, 0); i += kThreads) sh.y[i] = 0.f;  // selections of no expert stay zero
+  }
+  __device__ void run() {
+    if (R <= 0) return;
+    for (int u = warp; u < units; u += kWarps) {
+      const int g = u / tiles, r = (u - g * tiles) * kRows + (lane >> 2), n = sh.group_n[g];
+      const int mine = sh.member[g * kGroup + min(lane >> 2, n - 1)];
+      const size_t from = (size_t)mine * a.s + piece;
+      Sums<I8> c = {};
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll 2
+      for (int st = 0; st < steps; ++st) {
+        const int col = st * 4 * kVec;
+        const bool in = col + piece < a.s;
+        uint4 hi = zero, lo = zero;
+        if (in) {
+          if constexpr (I8) {
+            hi = *reinterpret_cast<const uint4*>(a.mid_q + from + col);
+          } else {
+            hi = *reinterpret_cast<const uint4*>(a.mid_hi + from + col);
+            lo = *reinterpret_cast<const uint4*>(a.mid_lo + from + col);
+          }
+        }
+        wait_oldest();
+        const uint32_t at = ring.drain();
+        const uint4 w0 = in && r < R ? sm100::ld_shared_v4(at) : zero;
+        const uint4 w1 = in && r + 8 < R ? sm100::ld_shared_v4(at + 512) : zero;
+        fetch();
+        step_products<I8>(c, w0, w1, hi);
+        if constexpr (!I8) step_products<I8>(c, w0, w1, lo);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = 2 * (lane & 3) + (q & 1), rr = r + (q >> 1) * 8;
+        if (col >= n || rr >= R) continue;
+        const int slot = sh.member[g * kGroup + col];
+        float y;
+        if constexpr (I8)
+          y = (float)c.v[q] * (a.mid_scale[slot] * a.down_scale[(size_t)sh.group_e[g] * a.h + o0 + rr]);
+        else
+          y = c.v[q];
+        sh.y[slot * R + rr] = y;
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.N * R; i += kThreads) {
+      const int n = i / R, r = i - n * R;
+      float sum = 0.f;
+      for (int j = 0; j < a.k; ++j) sum = fmaf(sh.gate[n * a.k + j], sh.y[(n * a.k + j) * R + r], sum);
+      a.out[(size_t)n * a.h + o0 + r] = __float2bfloat16_rn(sum);
+    }
+  }
+};
 
 template <bool I8>
-__device__ void down_phase(const LayerArgs& a, const Shared& sh, int groups, int rows_each) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int o0 = blockIdx.x * rows_each, R = min(rows_each, a.h - o0);  // this CTA's output channels
-  if (R <= 0) return;
-  for (int i = threadIdx.x; i < a.S * R; i += kThreads) sh.y[i] = 0.f;  // selections of no expert stay zero
-  if constexpr (I8) {
-    for (int i = warp; i < a.S; i += kWarps) {
-      float top = 0.f;
-      if (sh.expert[i] >= 0)
-        for (int c = lane * 4; c < a.s; c += 128) {
-          const float4 x = *reinterpret_cast<const float4*>(a.mid + (size_t)i * a.s + c);
-          top = fmaxf(fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
-        }
-#pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      if (lane == 0) sh.top[i] = top;
-    }
-  }
-  __syncthreads();
-  int L = 1;  // lanes a row
-  while (L < 32 && L * (I8 ? 16 : 8) < a.s) L <<= 1;
-  const int step = kRowBlocks * (32 / L), sets = (R + step - 1) / step;
-  for (int u = warp; u < groups * sets; u += kWarps) {
-    const int g = u / sets, r0 = (u - g * sets) * step, n = sh.group_n[g];
-#define MORE_CALL(TB) down_unit<I8, TB>(a, sh, g, n, o0, R, r0, L, lane)
-    MORE_BY_COUNT(n, MORE_CALL)
-#undef MORE_CALL
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.N * R; i += kThreads) {
-    const int n = i / R, r = i - n * R;
-    float sum = 0.f;
-    for (int j = 0; j < a.k; ++j) sum = fmaf(sh.gate[n * a.k + j], sh.y[(n * a.k + j) * R + r], sum);
-    a.out[(size_t)n * a.h + o0 + r] = __float2bfloat16_rn(sum);
-  }
-}
-
-constexpr int kSolo = 2;
-
-template <bool I8, int KCAP>
 __global__ void __launch_bounds__(kThreads, 1) layer_kernel(const LayerArgs a, int rows_each) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float part[kWarps][2 * kGroup];
-  __shared__ float pv[kWarps][KCAP];
-  __shared__ int pe[kWarps][KCAP];
-  __shared__ int counts[kWarps];
+  __shared__ union {
+    float part[kWarps][16];
+    Select select;
+    Sums<I8> red[2][kWarps][32];
+    float tops[kWarps];
+  } u;
+  __shared__ int warp_sums[kWarps];
   __shared__ int failed;
-  const Shared sh = shared_at(smem, a.S, rows_each);
+  const Shared sh = shared_at(smem, a.S);
   unsigned turn = 0;
-  project_tokens(a, part);
-  if constexpr (I8) round_tokens(a, &part[0][0]);
+  if constexpr (I8) round_tokens(a, u.tops);
+  project_tokens(a, u.part);
   if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
   expert_logits(a);
   if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
   const bool solo = a.N <= kSolo;
   if (solo) {
-    for (int n = 0; n < a.N; ++n) select_experts<KCAP>(a, n, pv, pe, sh.expert, sh.gate);
+    for (int n = 0; n < a.N; ++n) select_experts(a, n, u.select, sh.expert, sh.gate);
   } else {
-    for (int n = blockIdx.x; n < a.N; n += gridDim.x) select_experts<KCAP>(a, n, pv, pe, a.idx, a.gate);
+    for (int n = blockIdx.x; n < a.N; n += gridDim.x) select_experts(a, n, u.select, a.idx, a.gate);
     if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
   }
-  const int groups = group_selections(a, sh, solo, counts);
-  up_phase<I8>(a, sh, groups, part);
-  if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
-  down_phase<I8>(a, sh, groups, rows_each);
+  const int groups = group_selections(a, sh, solo, warp_sums);
+  up_phase<I8>(a, sh, groups, u.red);
+  if constexpr (I8) {
+    if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
+    round_middles(a, sh, u.tops);
+  }
+  Down<I8> down(a, sh, groups, rows_each);
+  down.start();
+  if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
+  down.run();
 }
 
 int sm_count() {
@@ -676,31 +811,30 @@ int sm_count() {
   return sms;
 }
 
-template <bool I8, int KCAP>
+template <bool I8>
 cudaError_t launch_layer(const LayerArgs& a, cudaStream_t stream) {
   const int grid = sm_count();
   const int rows_each = (a.h + grid - 1) / grid;
-  const uint32_t smem = layer_smem(a.S, rows_each);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   static std::atomic<int> done[64] = {};
   if (dev < 0 || dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(layer_kernel<I8, KCAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost);
+    e = cudaFuncSetAttribute(layer_kernel<I8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev].store(1, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = layer_smem(a.S, rows_each);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;  // every CTA waits for the others at the barriers
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, layer_kernel<I8, KCAP>, a, rows_each);
+  return cudaLaunchKernelEx(&cfg, layer_kernel<I8>, a, rows_each);
 }
 
 }  // namespace
@@ -708,7 +842,7 @@ cudaError_t launch_layer(const LayerArgs& a, cudaStream_t stream) {
 // The few-token kernel takes the shape: its shared memory holds the selections' output channels (a CTA's share of h,
 // at least 132 CTAs assumed), and a batch of up to kFewTokens tokens.
 bool layer_few_fits(int64_t N, int h, int k) {
-  return N <= kFewTokens && layer_smem((int)(N * k), (h + 131) / 132) <= kSmemMost - 2048;
+  return N <= kFewTokens && layer_smem((int)(N * k), (h + 131) / 132) <= kSmemMost;
 }
 
 cudaError_t launch_layer_few(const FewArgs& f) {
@@ -716,31 +850,34 @@ cudaError_t launch_layer_few(const FewArgs& f) {
   a.X = static_cast<const __nv_bfloat16*>(f.X);
   a.R1 = static_cast<const __nv_bfloat16*>(f.R1);
   a.R2 = static_cast<const __nv_bfloat16*>(f.R2);
-  a.z = f.z;
-  a.logits = f.logits;
-  a.r = f.r;
   a.Xq = f.Xq;
   a.x_scale = f.x_scale;
   a.W_up = f.W_up;
   a.W_down = f.W_down;
   a.up_scale = f.up_scale;
   a.down_scale = f.down_scale;
+  a.z = f.z;
+  a.logits = f.logits;
   a.idx = f.idx;
   a.gate = f.gate;
+  a.mid_hi = f.mid_pair;
+  a.mid_lo = f.mid_pair + f.N * f.k * f.s;
   a.mid = f.mid;
+  a.mid_q = f.mid_q;
+  a.mid_scale = f.mid_scale;
   a.out = static_cast<__nv_bfloat16*>(f.out);
   a.barrier = f.barrier;
   a.status = f.status;
   a.N = (int)f.N;
   a.h = f.h;
+  a.r = f.r;
   a.s = f.s;
   a.M = f.M;
   a.k = f.k;
   a.S = (int)(f.N * f.k);
   const cudaError_t e = cudaMemsetAsync(f.barrier, 0, sizeof(unsigned int), f.stream);
   if (e != cudaSuccess) return e;
-  if (a.k <= 8) return f.Xq ? launch_layer<true, 8>(a, f.stream) : launch_layer<false, 8>(a, f.stream);
-  return f.Xq ? launch_layer<true, 16>(a, f.stream) : launch_layer<false, 16>(a, f.stream);
+  return f.Xq ? launch_layer<true>(a, f.stream) : launch_layer<false>(a, f.stream);
 }
 
 }  // namespace more

@@ -40,7 +40,7 @@ def _middle(x, U_e, s, K):
 
 
 def forward(X, W_up, W_down, gate, offsets, slots, fp32_rows=False, up_scale=None, down_scale=None):
-    """(out, bound).  fp32_rows: the middle and the slots' rows stay fp32 (no rounding to bf16 before the sum)."""
+    """(out, bound).  fp32_rows: the middle is carried as a bf16 pair and the slots' rows in fp32."""
     X, gate = X.double(), gate.double()
     N, h = X.shape
     s, k = W_down.shape[2], gate.shape[1]
@@ -64,7 +64,8 @@ def forward(X, W_up, W_down, gate, offsets, slots, fp32_rows=False, up_scale=Non
             a, b, sg, m, ea, eb, em = _middle(x, A, s, h)
             y = m @ D.T
             mag = m.abs() @ D.abs().T
-            off = em @ D.abs().T + s * W * mag + (0 if fp32_rows else U * mag)
+            # fp32_rows: the middle as a bf16 pair; the second rounding is off by U of a remainder of at most U
+            off = em @ D.abs().T + s * W * mag + (U * U if fp32_rows else U) * mag
         off = off + (0 if fp32_rows else U * y.abs()) + 2 * W * y.abs()
         out.index_add_(0, of // k, g * y)
         bound.index_add_(0, of // k, g.abs() * (off + k * W * mag))
