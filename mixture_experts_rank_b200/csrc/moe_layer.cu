@@ -18,8 +18,8 @@
 // one instruction takes 512 bytes of weights, where a thread's own multiply-adds, with their conversions and the
 // reductions over lanes, took longer than the reading (N = 64, h = 2048, s = 64: 2.6 TB/s in step 5).  A product's terms may
 // come in any order as long as both operands keep to it, so a lane's 16 contiguous bytes of a row serve as its fragments of two
-// MMAs without any shuffling.  Weights pass through a ring of asynchronous copies of each warp's own, 7 KB a warp in
-// flight, that runs on from one group to the next.
+// MMAs without any shuffling.  Weights pass through rings of asynchronous copies, three quarters of each in flight, that run on from one group to the next; copies take 128 or 256 contiguous bytes of a row at a time
+// (64 at a time, in the MMA's own order, reached 4.8 TB/s where these reach more).
 //
 // z is carried as the bf16 pair of the routing kernels, and m as such a pair (about 16 bits), since B is bf16: two MMAs
 // where one would round m to 8 bits.  All sums are fp32.  With 8-bit weights sums are whole numbers and m is rounded to
@@ -40,11 +40,11 @@ constexpr int kGroup = 8;  // selections of one expert that share a reading of i
 constexpr int kRows = 16;  // rows of an MMA
 constexpr int64_t kFewTokens = 64;
 constexpr int kSolo = 2;         // tokens that every CTA routes for itself
-constexpr int kStages = 8;       // steps of a warp's ring
-constexpr uint32_t kEntry = 1024;  // a step: 16 rows x 64 bytes, two 16-byte pieces a lane
-constexpr uint32_t kRing = kWarps * kStages * kEntry;
+constexpr int kSlots = 4;                   // batches of a warp's ring
+constexpr uint32_t kRing = 128 * 1024;      // all warps' rings
 constexpr uint32_t kSmemMost = 200 * 1024;  // dynamic
-constexpr int kCandidates = 256;
+constexpr int kCandidates = 512;  // as many as threads: where there is no bound there may be that many logits
+constexpr int kHeld = 8;  // keys that a thread keeps in registers while a token's experts are chosen
 
 struct LayerArgs {
   const __nv_bfloat16 *X, *R1, *R2;
@@ -217,38 +217,52 @@ __device__ void round_tokens(const LayerArgs& a, float* warp_tops) {
   }
 }
 
-// Step 2.
-__device__ void expert_logits(const LayerArgs& a) {
+// Step 2.  `zs`: N r floats of shared memory.  A warp keeps its octet's weights while it goes through tokens.
+__device__ void expert_logits(const LayerArgs& a, float* zs) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < a.N * a.r; i += kThreads) zs[i] = a.z[i];
+  __syncthreads();
   const int octets = a.M / 8, mine = (octets - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
-  for (int u = warp; u < mine * a.N; u += kWarps) {
-    const int j = u / a.N, n = u - j * a.N;
+  // units: an octet's tokens in runs, so that few octets still fill the warps
+  const int runs = min(a.N, max(1, kWarps / max(mine, 1))), each = (a.N + runs - 1) / runs;
+  for (int u = warp; u < mine * runs; u += kWarps) {
+    const int j = u / runs, n0 = (u - j * runs) * each;
     const int e0 = 8 * ((int)blockIdx.x + (int)gridDim.x * j);
-    float acc[8];
+    uint4 w[4];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) acc[q] = 0.f;
-    for (int row = lane; row < a.r; row += 32) {
-      float x[8];
-      widen8(__ldg(reinterpret_cast<const uint4*>(a.R2 + (size_t)row * a.M + e0)), x);
-      const float zi = a.z[n * a.r + row];
+    for (int i = 0; i < 4; ++i)
+      w[i] = lane + 32 * i < a.r ? __ldg(reinterpret_cast<const uint4*>(a.R2 + (size_t)(lane + 32 * i) * a.M + e0))
+                                 : make_uint4(0, 0, 0, 0);
+#pragma unroll 2
+    for (int n = n0; n < min(a.N, n0 + each); ++n) {
+      float acc[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) acc[q] = fmaf(zi, x[q], acc[q]);
+      for (int q = 0; q < 8; ++q) acc[q] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (32 * i >= a.r) break;
+        float x[8];
+        widen8(w[i], x);
+        const float zi = lane + 32 * i < a.r ? zs[n * a.r + lane + 32 * i] : 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[q] = fmaf(zi, x[q], acc[q]);
+      }
+      const float v = reduce_scatter<8>(acc, lane);
+      if ((lane & 3) == 0) a.logits[(size_t)n * a.M + e0 + (lane >> 2)] = v;
     }
-    __syncwarp();
-    const float v = reduce_scatter<8>(acc, lane);
-    if ((lane & 3) == 0) a.logits[(size_t)n * a.M + e0 + (lane >> 2)] = v;
   }
 }
 
 // Step 3 for token n: its selections and gates at idx and gate (shared or global memory).
-//   Every thread's largest key is known at once; the k-th largest of those bounds the k-th largest logit from below.
-//   Twelve bits of that bound, a vote each, leave a handful of candidates, which rank one another in parallel: rounds of
-//   a block-wide largest value cost 200 cycles each, 16 of them for k = 8.  More candidates than kCandidates (logits that are
-//   all but equal) are thinned by the bound's other bits, and equal ones by their experts.
+//   The k-th largest of the 16 warps' largest keys bounds the k-th largest logit from below (fewer warps with logits than k:
+//   no bound).  It leaves a handful of candidates, which rank one another in parallel: rounds of a block-wide largest value
+//   cost 200 cycles each, 16 of them for k = 8.  More candidates than kCandidates (logits that are all but equal) are
+//   thinned by bisection, equal ones by their experts.
 struct Select {
   uint32_t key[kCandidates];
   int expert[kCandidates];
   float value[MORE_KMAX];
+  uint32_t top[kWarps];
   int count;
 };
 
@@ -259,88 +273,104 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 __device__ void select_experts(const LayerArgs& a, int n, Select& s, int32_t* idx, float* gate) {
   const float* l = a.logits + (size_t)n * a.M;
   uint32_t top = 0;  // below every number's key; a NaN logit is never chosen
-  for (int e = threadIdx.x; e < a.M; e += kThreads) {
-    const float v = l[e];
-    if (v == v) top = max(top, key_of(v));
+  uint32_t held[kHeld];  // this thread's first keys
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int e = threadIdx.x + i * kThreads;
+    const float v = e < a.M ? l[e] : NAN;
+    held[i] = v == v ? key_of(v) : 0;
   }
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) top = max(top, held[i]);
+#pragma unroll 4
+  for (int e = threadIdx.x + kHeld * kThreads; e < a.M; e += kThreads) {
+    const float v = l[e];
+    top = max(top, v == v ? key_of(v) : 0);
+  }
+  const uint32_t warp_top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) s.top[threadIdx.x >> 5] = warp_top;
+  __syncthreads();
   uint32_t bound = 0;
-  int bit = 31;
+  if (a.k <= kWarps) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t mine = lane < kWarps ? s.top[lane] : 0;
+    int rank = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const uint32_t o = s.top[w];
+      rank += o > mine || (o == mine && w < lane);
+    }
+    const unsigned at = __ballot_sync(0xffffffffu, lane < kWarps && rank == a.k - 1);
+    bound = __shfl_sync(0xffffffffu, mine, __ffs(at) - 1);
+  }
   int limit = 0x7fffffff;  // candidates at the bound itself: only experts below this
   auto collect = [&]() {
-    __syncthreads();
     if (threadIdx.x == 0) s.count = 0;
     __syncthreads();
-    for (int e = threadIdx.x; e < a.M; e += kThreads) {
-      const float v = l[e];
-      const uint32_t key = key_of(v);
-      if (v == v && key >= bound && (key > bound || e < limit)) {
+    auto take = [&](uint32_t key, int e) {
+      if (key != 0 && key >= bound && (key > bound || e < limit)) {
         const int at = atomicAdd(&s.count, 1);
         if (at < kCandidates) {
           s.key[at] = key;
           s.expert[at] = e;
         }
       }
+    };
+    if (top >= bound) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) take(held[i], threadIdx.x + i * kThreads);
+#pragma unroll 1
+      for (int e = threadIdx.x + kHeld * kThreads; e < a.M; e += kThreads) {
+        const float v = l[e];
+        take(v == v ? key_of(v) : 0, e);
+      }
     }
     __syncthreads();
     return s.count;
   };
-  auto refine = [&](int last) {
-    for (; bit >= last; --bit) {
-      const uint32_t trial = bound | 1u << bit;
-      if (__syncthreads_count(top >= trial) >= a.k) bound = trial;
-    }
-  };
-  refine(20);
   int count = collect();
   if (count > kCandidates) {
-    refine(0);
-    count = collect();
-    if (count > kCandidates) {
-      // The bound is some thread's largest key, reached by at least k of them, so fewer than k threads hold a larger
-      // key, but those may hold many, and so may the ties.  First the larger keys alone, if they suffice, else the
-      // lowest experts of the ties beside them: both by bisection.
-      uint32_t lo = bound, hi = 0xffffffffu;  // at least k keys >= lo; find the largest such lo
-      while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo) / 2 + 1;
-        int c = 0;
-        for (int e = threadIdx.x; e < a.M; e += kThreads) {
-          const float v = l[e];
-          c += v == v && key_of(v) >= mid;
-        }
-        // a thread counts as many as it has, up to k
-        int total = 0;
-        for (int j = 0; j < a.k; ++j) total += __syncthreads_count(c > j);
-        if (total >= a.k)
-          lo = mid;
-        else
-          hi = mid - 1;
+    uint32_t lo = bound, hi = 0xffffffffu;  // the largest lo with at least k keys at or above it: the k-th largest key
+    while (lo < hi) {
+      const uint32_t mid = lo + (hi - lo) / 2 + 1;
+      int c = 0;
+      for (int e = threadIdx.x; e < a.M; e += kThreads) {
+        const float v = l[e];
+        c += v == v && key_of(v) >= mid;
       }
-      bound = lo;  // the k-th largest key itself: fewer than k are larger
-      int from = 0, to = a.M;  // the first experts [0, to) hold k keys at or above it
-      while (from < to) {
-        const int half = (from + to) / 2;
-        int c = 0;
-        for (int e = threadIdx.x; e < a.M; e += kThreads) {
-          const float v = l[e];
-          const uint32_t key = key_of(v);
-          c += v == v && (key > bound || (key == bound && e < half));
-        }
-        int total = 0;
-        for (int j = 0; j < a.k; ++j) total += __syncthreads_count(c > j);
-        if (total >= a.k)
-          to = half;
-        else
-          from = half + 1;
-      }
-      limit = to;
-      count = collect();
+      int total = 0;  // a thread counts as many as it has, up to k
+      for (int j = 0; j < a.k; ++j) total += __syncthreads_count(c > j);
+      if (total >= a.k)
+        lo = mid;
+      else
+        hi = mid - 1;
     }
+    bound = lo;
+    int from = 0, to = a.M;  // the fewest first experts [0, to) whose ties, with the larger keys, make k
+    while (from < to) {
+      const int half = (from + to) / 2;
+      int c = 0;
+      for (int e = threadIdx.x; e < a.M; e += kThreads) {
+        const float v = l[e];
+        const uint32_t key = key_of(v);
+        c += v == v && (key > bound || (key == bound && e < half));
+      }
+      int total = 0;
+      for (int j = 0; j < a.k; ++j) total += __syncthreads_count(c > j);
+      if (total >= a.k)
+        to = half;
+      else
+        from = half + 1;
+    }
+    limit = to;
+    count = collect();
   }
   // ranks
   for (int c = threadIdx.x; c < count; c += kThreads) {
     const uint32_t key = s.key[c];
     const int e = s.expert[c];
     int rank = 0;
+#pragma unroll 4
     for (int o = 0; o < count; ++o) rank += s.key[o] > key || (s.key[o] == key && s.expert[o] < e);
     if (rank < a.k) {
       s.value[rank] = value_of(key);
@@ -386,6 +416,36 @@ __device__ int group_selections(const LayerArgs& a, const Shared& sh, bool solo,
   int32_t* t_first = t_count + kTable;
   int32_t* t_base = t_first + kTable;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (a.S <= 32) {  // one warp's lanes find one another
+    if (warp == 0) {
+      int e = lane < a.S ? (solo ? sh.expert[lane] : a.idx[lane]) : -1;
+      if (!solo && lane < a.S) sh.gate[lane] = a.gate[lane];
+      const bool ok = e >= 0 && e < a.M;
+      if (!ok && lane < a.S && blockIdx.x == 0) atomicOr(a.status, MORE_DEVERR_BAD_INPUT);
+      if (!ok) e = -1;
+      if (lane < a.S) sh.expert[lane] = e;
+      const unsigned same = __match_any_sync(0xffffffffu, e);
+      const int nth = __popc(same & ((1u << lane) - 1)), count = __popc(same), first = __ffs(same) - 1;
+      int sum = ok && nth == 0 ? (count + kGroup - 1) / kGroup : 0;
+      const int mine = sum;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += o;
+      }
+      const int g = __shfl_sync(0xffffffffu, sum - mine, first) + nth / kGroup;
+      if (ok) {
+        sh.member[g * kGroup + nth % kGroup] = (int16_t)lane;
+        if (nth % kGroup == 0) {
+          sh.group_e[g] = e;
+          sh.group_n[g] = min(kGroup, count - nth);
+        }
+      }
+      if (lane == 31) warp_sums[0] = sum;
+    }
+    __syncthreads();
+    return warp_sums[0];
+  }
   for (int i = threadIdx.x; i < kTable; i += kThreads) {
     t_expert[i] = -1;
     t_count[i] = 0;
@@ -456,11 +516,6 @@ __device__ int group_selections(const LayerArgs& a, const Shared& sh, bool solo,
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// With kStages - 1 steps in flight: waits for the oldest.
-__device__ __forceinline__ void wait_oldest() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-}
 
 template <bool I8>
 struct Sums {
@@ -492,20 +547,34 @@ __device__ __forceinline__ void step_products(Sums<I8>& c, uint4 w0, uint4 w1, u
   mma(c, w0.z, w1.z, w0.w, w1.w, x.z, x.w);
 }
 
-// A warp's ring: steps are fetched kStages - 1 ahead, in the order that `Next` gives them.
-struct RingAt {
-  uint32_t base;  // of this lane's pieces
+// A warp's ring of batches: 16 rows x BS steps of 64 bytes, fetched kSlots - 1 batches ahead.  A row's 16-byte pieces lie
+// together, those of odd rows with their halves of 64 bytes swapped: eight lanes of two rows then read all 32 banks.
+template <int BS>
+struct Ring {
+  static constexpr int kStreams = 32 / BS;      // warps: 16 with batches of 2 KB, 8 with batches of 4 KB
+  static constexpr uint32_t kBatch = 64 * BS;   // bytes of a row
+  static constexpr uint32_t kBytes = kSlots * 16 * kBatch;
+  static_assert(kStreams * kBytes == kRing && kStreams <= kWarps, "rings");
+  static constexpr int kPieces = 4 * BS;       // lanes a row
+  static constexpr int kAtOnce = 32 / kPieces;  // rows a copy instruction
+  uint32_t base;
   int in = 0, out = 0;
   __device__ __forceinline__ uint32_t fill() {
-    const uint32_t at = base + in * kEntry;
-    in = (in + 1) & (kStages - 1);
+    const uint32_t at = base + in * 16 * kBatch;
+    in = (in + 1) & (kSlots - 1);
     return at;
   }
+  // The oldest batch, landed and seen by every lane; the batch before it may be overwritten from here on.
   __device__ __forceinline__ uint32_t drain() {
-    const uint32_t at = base + out * kEntry;
-    out = (out + 1) & (kStages - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
+    __syncwarp();
+    const uint32_t at = base + out * 16 * kBatch;
+    out = (out + 1) & (kSlots - 1);
     return at;
   }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // Where piece p of row r is.
+  static __device__ __forceinline__ uint32_t place(int r, int p) { return r * kBatch + ((p ^ ((r & 1) << 2)) << 4); }
 };
 
 __device__ __forceinline__ float silu_times(float a, float b) { return a * __fdividef(1.f, 1.f + expf(-a)) * b; }
@@ -542,92 +611,130 @@ __device__ __forceinline__ void finish_up(const LayerArgs& a, const Shared& sh, 
   }
 }
 
-// Step 4.  Unit u: rows 8 (u % (s / 8)) on of group u / (s / 8).  `parts` warps a unit, each a run of its steps.
+// Step 4.  Unit u: rows 8 (u % (s / 8)) on of group u / (s / 8).  `parts` warps a unit, each a run of its batches.
+constexpr int kUpStreams = Ring<4>::kStreams;
+
 template <bool I8>
-__device__ void up_phase(const LayerArgs& a, const Shared& sh, int groups, Sums<I8> (*red)[kWarps][32]) {
-  constexpr int kBytes = I8 ? 1 : 2, kVec = 16 / kBytes;
+__device__ void up_phase(const LayerArgs& a, const Shared& sh, int groups, Sums<I8> (*red)[kUpStreams][32]) {
+  constexpr int BS = 4;
+  using R = Ring<BS>;
+  constexpr int kStreams = R::kStreams;
+  constexpr int kBytes = I8 ? 1 : 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int eights = a.s / 8, units = groups * eights, steps = (a.h + 4 * kVec - 1) / (4 * kVec);
-  // The fewest steps a warp, a round's end counted as two more: rounds of all warps' units, shorter with more parts.
+  const int eights = a.s / 8, units = groups * eights;
+  const int pitch = a.h * kBytes, batches = (pitch + (int)R::kBatch - 1) / (int)R::kBatch;
+  // The fewest batches a warp, a round's end counted as half a one: rounds of all warps' units, shorter with more parts.
   int parts = 1, best = 0x7fffffff;
-  for (int p = 1; p <= kWarps; p *= 2) {
-    const int per_round = (int)gridDim.x * (kWarps / p), rounds = (units + per_round - 1) / per_round;
-    const int cost = rounds * ((steps + p - 1) / p + (p > 1 ? 2 : 0));
+  for (int p = 1; p <= kStreams; p *= 2) {
+    const int per_round = (int)gridDim.x * (kStreams / p), rounds = (units + per_round - 1) / per_round;
+    const int cost = rounds * (2 * ((batches + p - 1) / p) + (p > 1 ? 1 : 0));
     if (cost < best) {
       best = cost;
       parts = p;
     }
   }
-  const int each = kWarps / parts, stride = (int)gridDim.x * each;
-  const int first = (int)blockIdx.x * each, part = warp % parts;
-  const int s0 = steps * part / parts, s1 = steps * (part + 1) / parts;
-  const int piece = (lane & 3) * kVec;
-  const size_t to_b = (size_t)a.s * a.h * kBytes;
-  RingAt ring{sh.ring + warp * kStages * kEntry + lane * 16};
-  // what is fetched next
-  int fu = first + warp / parts, fs = s0;
-  const uint8_t* row = nullptr;
+  const int each = kStreams / parts, stride = (int)gridDim.x * each, first = (int)blockIdx.x * each;
+  const bool streams = warp < kStreams;
+  const int part = warp % parts, b0 = batches * part / parts, b1 = streams ? batches * (part + 1) / parts : b0;
+  R ring{sh.ring + (uint32_t)warp * R::kBytes};
+  // copies: this lane's piece and its rows
+  const int pc = lane % R::kPieces, r0 = lane / R::kPieces;
+  const uint32_t dst = R::place(r0, pc);  // kAtOnce is even: the lane's rows are all odd or all even
+  const size_t to_b = (size_t)(a.s - 8) * pitch;
+  int fu = first + warp / parts, fb = b0;
+  const uint8_t* from = nullptr;
   auto locate = [&]() {
     if (fu >= units) return;
-    const int g = fu / eights, i = (fu - g * eights) * 8 + (lane >> 2);
-    row = static_cast<const uint8_t*>(a.W_up) + (((size_t)sh.group_e[g] * 2 * a.s + i) * a.h + piece) * kBytes;
+    const int g = fu / eights;
+    from = static_cast<const uint8_t*>(a.W_up) +
+           ((size_t)sh.group_e[g] * 2 * a.s + (fu - g * eights) * 8 + r0) * pitch + pc * 16;
   };
   locate();
   auto fetch = [&]() {
-    const uint32_t at = ring.fill();
-    if (fu < units && s0 < s1) {
-      const int col = fs * 4 * kVec;
-      if (col + piece < a.h) {
-        copy16(at, row + (size_t)col * kBytes);
-        copy16(at + 512, row + to_b + (size_t)col * kBytes);
+    const uint32_t at = ring.fill() + dst;
+    if (b0 < b1 && fu < units) {
+      const int off = fb * (int)R::kBatch;
+      if (off + pc * 16 < pitch) {
+#pragma unroll
+        for (int i = 0; i < 16 / R::kAtOnce; ++i)
+          copy16(at + i * R::kAtOnce * R::kBatch,
+                 from + off + (size_t)i * R::kAtOnce * pitch + (i * R::kAtOnce >= 8 ? to_b : 0));
       }
-      if (++fs == s1) {
-        fs = s0;
+      if (++fb == b1) {
+        fb = b0;
         fu += stride;
         locate();
       }
     }
-    commit_copies();
+    R::commit();
   };
+  if (streams) {
 #pragma unroll 1
-  for (int i = 0; i < kStages - 1; ++i) fetch();
+    for (int i = 0; i < kSlots - 1; ++i) fetch();
+  }
+  // products: this lane's row and 16 bytes of each step
+  const int row = lane >> 2, piece = (lane & 3) * 16;
+  const uint8_t* X = I8 ? reinterpret_cast<const uint8_t*>(a.Xq) : reinterpret_cast<const uint8_t*>(a.X);
+  auto token_at = [&](int u) {
+    const int g = u / eights;
+    return X + (size_t)(sh.member[g * kGroup + min(row, sh.group_n[g] - 1)] / a.k) * pitch + piece;
+  };
+  uint4 x[BS], ahead[BS];
+  auto load_x = [&](const uint8_t* p, int b, uint4 (&to)[BS]) {
+#pragma unroll
+    for (int j = 0; j < BS; ++j) {
+      const int off = b * (int)R::kBatch + 64 * j;
+      to[j] = off + piece < pitch ? *reinterpret_cast<const uint4*>(p + off) : make_uint4(0, 0, 0, 0);
+    }
+  };
   int parity = 0;
+  const uint8_t* p = nullptr;
+  if (first + warp / parts < units && b0 < b1) {
+    p = token_at(first + warp / parts);
+    load_x(p, b0, ahead);
+  }
+#pragma unroll 1
   for (int u0 = first; u0 < units; u0 += stride) {
     const int u = u0 + warp / parts;
     Sums<I8> c = {};
-    int g = 0, i = 0;
-    if (u < units) {
-      g = u / eights;
-      i = (u - g * eights) * 8 + (lane >> 2);
-      const int tok = sh.member[g * kGroup + min(lane >> 2, sh.group_n[g] - 1)] / a.k;
-      const uint8_t* x = (I8 ? reinterpret_cast<const uint8_t*>(a.Xq) : reinterpret_cast<const uint8_t*>(a.X)) +
-                         ((size_t)tok * a.h + piece) * kBytes;
-#pragma unroll 2
-      for (int st = s0; st < s1; ++st) {
-        const int col = st * 4 * kVec;
-        const bool in = col + piece < a.h;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        const uint4 xv = in ? *reinterpret_cast<const uint4*>(x + (size_t)col * kBytes) : zero;
-        wait_oldest();
-        const uint32_t at = ring.drain();
-        const uint4 w0 = in ? sm100::ld_shared_v4(at) : zero, w1 = in ? sm100::ld_shared_v4(at + 512) : zero;
+    if (streams && u < units) {
+#pragma unroll 1
+      for (int b = b0; b < b1; ++b) {
+#pragma unroll
+        for (int j = 0; j < BS; ++j) x[j] = ahead[j];
+        if (b + 1 < b1) {
+          load_x(p, b + 1, ahead);
+        } else if (u + stride < units) {
+          p = token_at(u + stride);
+          load_x(p, b0, ahead);
+        }
+        const uint32_t at = ring.drain() + row * R::kBatch;
         fetch();
-        step_products<I8>(c, w0, w1, xv);
+#pragma unroll
+        for (int j = 0; j < BS; ++j) {
+          const uint32_t q = (uint32_t)(piece + 64 * j) ^ ((row & 1) << 6);
+          const bool in = b * (int)R::kBatch + 64 * j + piece < pitch;
+          uint4 w0 = sm100::ld_shared_v4(at + q), w1 = sm100::ld_shared_v4(at + 8 * R::kBatch + q);
+          if (!in) w0 = w1 = make_uint4(0, 0, 0, 0);
+          step_products<I8>(c, w0, w1, x[j]);
+        }
+      }
+      if (parts == 1) {
+        const int g = u / eights;
+        finish_up<I8>(a, sh, g, (u - g * eights) * 8 + row, lane, c);
       }
     }
-    if (parts == 1) {
-      if (u < units) finish_up<I8>(a, sh, g, i, lane, c);
-    } else {
-      red[parity][warp][lane] = c;
+    if (parts > 1) {
+      if (streams) red[parity][warp][lane] = c;
       __syncthreads();
       const int ur = u0 + warp;  // warp w sums unit w of the round
       if (warp < each && ur < units) {
         Sums<I8> t = red[parity][warp * parts][lane];
-        for (int p = 1; p < parts; ++p)
+        for (int q = 1; q < parts; ++q)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) t.v[q] += red[parity][warp * parts + p][lane].v[q];
-        const int gr = ur / eights;
-        finish_up<I8>(a, sh, gr, (ur - gr * eights) * 8 + (lane >> 2), lane, t);
+          for (int v = 0; v < 4; ++v) t.v[v] += red[parity][warp * parts + q][lane].v[v];
+        const int g = ur / eights;
+        finish_up<I8>(a, sh, g, (ur - g * eights) * 8 + row, lane, t);
       }
       parity ^= 1;
     }
@@ -660,109 +767,156 @@ __device__ void round_middles(const LayerArgs& a, const Shared& sh, float* warp_
   }
 }
 
-// Step 5.  Unit u: rows 16 (u % tiles) on of this CTA's for group u / tiles.  The first steps' copies start before the
-// barrier: they need the groups alone.
-template <bool I8>
+// Step 5.  Unit u: rows 16 (u % tiles) on of this CTA's for group u / tiles.  The first batches' copies start before
+// the barrier: they need the groups alone.
+template <bool I8, int BS>
 struct Down {
-  static constexpr int kBytes = I8 ? 1 : 2, kVec = 16 / kBytes;
+  using R = Ring<BS>;
+  static constexpr int kBytes = I8 ? 1 : 2;
   const LayerArgs& a;
   const Shared& sh;
-  int o0, R, tiles, units, steps, piece, lane, warp;
-  RingAt ring;
-  int fu, fs;
-  const uint8_t* row;
+  int o0, rows, tiles, units, batches, pitch, lane, warp, pc, r0;
+  R ring;
+  int fu, fb;
+  const uint8_t* from;
 
   __device__ Down(const LayerArgs& a_, const Shared& sh_, int groups, int rows_each) : a(a_), sh(sh_) {
     warp = threadIdx.x >> 5;
     lane = threadIdx.x & 31;
     o0 = blockIdx.x * rows_each;
-    R = min(rows_each, a.h - o0);
-    tiles = R > 0 ? (R + kRows - 1) / kRows : 0;
-    units = groups * tiles;
-    steps = (a.s + 4 * kVec - 1) / (4 * kVec);
-    piece = (lane & 3) * kVec;
-    ring.base = sh.ring + warp * kStages * kEntry + lane * 16;
+    rows = max(0, min(rows_each, a.h - o0));
+    tiles = (rows + kRows - 1) / kRows;
+    units = warp < R::kStreams ? groups * tiles : 0;
+    pitch = a.s * kBytes;
+    batches = (pitch + (int)R::kBatch - 1) / (int)R::kBatch;
+    pc = lane % R::kPieces;
+    r0 = lane / R::kPieces;
+    ring.base = sh.ring + (uint32_t)warp * R::kBytes;
     fu = warp;
-    fs = 0;
+    fb = 0;
     locate();
   }
   __device__ __forceinline__ void locate() {
     if (fu >= units) return;
-    const int g = fu / tiles, r = (fu - g * tiles) * kRows + (lane >> 2);
-    row = static_cast<const uint8_t*>(a.W_down) + (((size_t)sh.group_e[g] * a.h + o0 + r) * a.s + piece) * kBytes;
+    const int g = fu / tiles, r = (fu - g * tiles) * kRows + r0;
+    from = static_cast<const uint8_t*>(a.W_down) + ((size_t)sh.group_e[g] * a.h + o0 + r) * pitch + pc * 16;
   }
   __device__ __forceinline__ void fetch() {
-    const uint32_t at = ring.fill();
+    const uint32_t at = ring.fill() + R::place(r0, pc);
     if (fu < units) {
-      const int col = fs * 4 * kVec, r = fu % tiles * kRows + (lane >> 2);
-      if (col + piece < a.s) {
-        if (r < R) copy16(at, row + (size_t)col * kBytes);
-        if (r + 8 < R) copy16(at + 512, row + ((size_t)8 * a.s + col) * kBytes);
+      const int off = fb * (int)R::kBatch, left = rows - fu % tiles * kRows - r0;
+      if (off + pc * 16 < pitch) {
+#pragma unroll
+        for (int i = 0; i < 16 / R::kAtOnce; ++i)
+          if (i * R::kAtOnce < left)
+            copy16(at + i * R::kAtOnce * R::kBatch, from + off + (size_t)i * R::kAtOnce * pitch);
       }
-      if (++fs == steps) {
-        fs = 0;
-        fu += kWarps;
+      if (++fb == batches) {
+        fb = 0;
+        fu += R::kStreams;
         locate();
       }
     }
-    commit_copies();
+    R::commit();
   }
   __device__ void start() {
+    if (warp < R::kStreams) {
 #pragma unroll 1
-    for (int i = 0; i < kStages - 1; ++i) fetch();
-    for (int i = threadIdx.x; i < a.S * max(R, 0); i += kThreads) sh.y[i] = 0.f;  // selections of no expert stay zero
+      for (int i = 0; i < kSlots - 1; ++i) fetch();
+    }
+    for (int i = threadIdx.x; i < a.S * rows; i += kThreads) sh.y[i] = 0.f;  // selections of no expert stay zero
+  }
+  __device__ __forceinline__ size_t middle_of(int u) const {
+    const int g = u / tiles;
+    return (size_t)sh.member[g * kGroup + min(lane >> 2, sh.group_n[g] - 1)] * pitch + (lane & 3) * 16;
+  }
+  __device__ __forceinline__ void load(size_t at, int b, uint4 (&hi)[BS], uint4 (&lo)[BS]) const {
+#pragma unroll
+    for (int j = 0; j < BS; ++j) {
+      const int off = b * (int)R::kBatch + 64 * j;
+      hi[j] = lo[j] = make_uint4(0, 0, 0, 0);
+      if (off + (lane & 3) * 16 < pitch) {
+        if constexpr (I8) {
+          hi[j] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(a.mid_q) + at + off);
+        } else {
+          hi[j] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(a.mid_hi) + at + off);
+          lo[j] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(a.mid_lo) + at + off);
+        }
+      }
+    }
   }
   __device__ void run() {
-    if (R <= 0) return;
-    for (int u = warp; u < units; u += kWarps) {
-      const int g = u / tiles, r = (u - g * tiles) * kRows + (lane >> 2), n = sh.group_n[g];
-      const int mine = sh.member[g * kGroup + min(lane >> 2, n - 1)];
-      const size_t from = (size_t)mine * a.s + piece;
+    const int row = lane >> 2, piece = (lane & 3) * 16;
+    uint4 hi[BS], lo[BS], next_hi[BS], next_lo[BS];
+    size_t mid = 0;
+    if (warp < units) {
+      mid = middle_of(warp);
+      load(mid, 0, next_hi, next_lo);
+    }
+#pragma unroll 1
+    for (int u = warp; u < units; u += R::kStreams) {
+      const int g = u / tiles, r = (u - g * tiles) * kRows + row, n = sh.group_n[g];
       Sums<I8> c = {};
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 2
-      for (int st = 0; st < steps; ++st) {
-        const int col = st * 4 * kVec;
-        const bool in = col + piece < a.s;
-        uint4 hi = zero, lo = zero;
-        if (in) {
-          if constexpr (I8) {
-            hi = *reinterpret_cast<const uint4*>(a.mid_q + from + col);
-          } else {
-            hi = *reinterpret_cast<const uint4*>(a.mid_hi + from + col);
-            lo = *reinterpret_cast<const uint4*>(a.mid_lo + from + col);
-          }
+#pragma unroll 1
+      for (int b = 0; b < batches; ++b) {
+#pragma unroll
+        for (int j = 0; j < BS; ++j) {
+          hi[j] = next_hi[j];
+          lo[j] = next_lo[j];
         }
-        wait_oldest();
-        const uint32_t at = ring.drain();
-        const uint4 w0 = in && r < R ? sm100::ld_shared_v4(at) : zero;
-        const uint4 w1 = in && r + 8 < R ? sm100::ld_shared_v4(at + 512) : zero;
+        if (b + 1 < batches) {
+          load(mid, b + 1, next_hi, next_lo);
+        } else if (u + R::kStreams < units) {
+          mid = middle_of(u + R::kStreams);
+          load(mid, 0, next_hi, next_lo);
+        }
+        const uint32_t at = ring.drain() + row * R::kBatch;
         fetch();
-        step_products<I8>(c, w0, w1, hi);
-        if constexpr (!I8) step_products<I8>(c, w0, w1, lo);
+#pragma unroll
+        for (int j = 0; j < BS; ++j) {
+          const uint32_t q = (uint32_t)(piece + 64 * j) ^ ((row & 1) << 6);
+          const bool in = b * (int)R::kBatch + 64 * j + piece < pitch;
+          uint4 w0 = sm100::ld_shared_v4(at + q), w1 = sm100::ld_shared_v4(at + 8 * R::kBatch + q);
+          if (!in || r >= rows) w0 = make_uint4(0, 0, 0, 0);
+          if (!in || r + 8 >= rows) w1 = make_uint4(0, 0, 0, 0);
+          step_products<I8>(c, w0, w1, hi[j]);
+          if constexpr (!I8) step_products<I8>(c, w0, w1, lo[j]);
+        }
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int col = 2 * (lane & 3) + (q & 1), rr = r + (q >> 1) * 8;
-        if (col >= n || rr >= R) continue;
+        if (col >= n || rr >= rows) continue;
         const int slot = sh.member[g * kGroup + col];
         float y;
         if constexpr (I8)
           y = (float)c.v[q] * (a.mid_scale[slot] * a.down_scale[(size_t)sh.group_e[g] * a.h + o0 + rr]);
         else
           y = c.v[q];
-        sh.y[slot * R + rr] = y;
+        sh.y[slot * rows + rr] = y;
       }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.N * R; i += kThreads) {
-      const int n = i / R, r = i - n * R;
+    for (int i = threadIdx.x; i < a.N * rows; i += kThreads) {
+      const int n = i / rows, r = i - n * rows;
       float sum = 0.f;
-      for (int j = 0; j < a.k; ++j) sum = fmaf(sh.gate[n * a.k + j], sh.y[(n * a.k + j) * R + r], sum);
+      for (int j = 0; j < a.k; ++j) sum = fmaf(sh.gate[n * a.k + j], sh.y[(n * a.k + j) * rows + r], sum);
       a.out[(size_t)n * a.h + o0 + r] = __float2bfloat16_rn(sum);
     }
   }
 };
+
+template <bool I8, int BS>
+__device__ __forceinline__ void down_phase(const LayerArgs& a, const Shared& sh, int groups, int rows_each,
+                                           unsigned turn, int* failed) {
+  __syncthreads();  // other warps' rings of the first product lie in this one's
+  Down<I8, BS> down(a, sh, groups, rows_each);
+  down.start();
+  if (grid_barrier(a.barrier, turn, a.status, failed))
+    down.run();
+  else
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
 
 template <bool I8>
 __global__ void __launch_bounds__(kThreads, 1) layer_kernel(const LayerArgs a, int rows_each) {
@@ -770,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_kernel(const LayerArgs a, i
   __shared__ union {
     float part[kWarps][16];
     Select select;
-    Sums<I8> red[2][kWarps][32];
+    Sums<I8> red[2][kUpStreams][32];
     float tops[kWarps];
   } u;
   __shared__ int warp_sums[kWarps];
@@ -780,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_kernel(const LayerArgs a, i
   if constexpr (I8) round_tokens(a, u.tops);
   project_tokens(a, u.part);
   if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
-  expert_logits(a);
+  expert_logits(a, reinterpret_cast<float*>(sh.work));
   if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
   const bool solo = a.N <= kSolo;
   if (solo) {
@@ -795,13 +949,11 @@ __global__ void __launch_bounds__(kThreads, 1) layer_kernel(const LayerArgs a, i
     if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
     round_middles(a, sh, u.tops);
   }
-  Down<I8> down(a, sh, groups, rows_each);
-  down.start();
-  if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) {
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    return;
-  }
-  down.run();
+  // rows of up to 128 bytes fill the ring in batches of two steps, longer ones in batches of four
+  if (a.s * (I8 ? 1 : 2) <= 128)
+    down_phase<I8, 2>(a, sh, groups, rows_each, ++turn, &failed);
+  else
+    down_phase<I8, 4>(a, sh, groups, rows_each, ++turn, &failed);
 }
 
 int sm_count() {
