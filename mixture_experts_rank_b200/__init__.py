@@ -109,7 +109,7 @@ def abi_version() -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream_handle(stream) -> ctypes.c_void_p:
@@ -308,12 +308,13 @@ _HERE = _Here()
 def _on_device(first: torch.Tensor, stream, **tensors):
     """Checks that every tensor lies on the device of ``first``; the context in which the call runs there, on the given
     stream or that device's current one."""
-    device = first.device
+    index = first.get_device()
     for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, {device} was expected")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, {first.device} was expected")
+    device = first.device
     if stream is None:
-        if device.index == torch.cuda.current_device():
+        if index == torch.cuda.current_device():
             return _HERE
         stream = torch.cuda.current_stream(device)
     elif stream.device != device:
@@ -324,7 +325,7 @@ def _on_device(first: torch.Tensor, stream, **tensors):
 def _typed(t, name, dtype, shape):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if not t.is_cuda or not t.is_contiguous() or t.shape != shape:
         raise ValueError(f"{name} must be a contiguous CUDA tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
@@ -375,7 +376,7 @@ def experts(X: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tensor, gate: tor
         out = _output(out, "out", torch.bfloat16, (N, h), X.device)
         scratch = _scratch(scratch, experts_scratch_bytes(N, h, s, M, k), X.device)
         st = _lib.more_experts(_ptr(X), _ptr(W_up), _ptr(W_down), N, h, s, M, k, _ptr(gate), _ptr(offsets),
-                               _ptr(slots), _ptr(out), _ptr(scratch), scratch.numel(), _stream_handle(None))
+                               _ptr(slots), _ptr(out), _ptr(scratch), scratch.numel(), torch._C._cuda_getCurrentRawStream(X.get_device()))
     _check(st, "more_experts")
     return out
 
@@ -393,7 +394,7 @@ def quantize_rows(V: torch.Tensor, *, out_q=None, out_scale=None, stream=None) -
         out_scale = _output(out_scale, "out_scale", torch.float32, V.shape[:-1], V.device)
         width = V.shape[-1]
         st = _lib.more_quantize_rows(_ptr(V), V.numel() // max(width, 1), width, _ptr(out_q), _ptr(out_scale),
-                                     _stream_handle(None))
+                                     torch._C._cuda_getCurrentRawStream(V.get_device()))
     _check(st, "more_quantize_rows")
     return out_q, out_scale
 
@@ -418,7 +419,7 @@ def experts_int8(X: torch.Tensor, W_up: torch.Tensor, up_scale: torch.Tensor, W_
         scratch = _scratch(scratch, experts_int8_scratch_bytes(N, h, s, M, k), X.device)
         st = _lib.more_experts_int8(_ptr(X), _ptr(W_up), _ptr(up_scale), _ptr(W_down), _ptr(down_scale), N, h, s, M, k,
                                     _ptr(gate), _ptr(offsets), _ptr(slots), _ptr(out), _ptr(scratch), scratch.numel(),
-                                    _stream_handle(None))
+                                    torch._C._cuda_getCurrentRawStream(X.get_device()))
     _check(st, "more_experts_int8")
     return out
 
@@ -451,7 +452,7 @@ def experts_backward(X: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tensor, 
         scratch = _scratch(scratch, experts_backward_scratch_bytes(N, h, s, M, k), X.device)
         st = _lib.more_experts_backward(_ptr(X), _ptr(W_up), _ptr(W_down), N, h, s, M, k, _ptr(gate), _ptr(offsets),
                                         _ptr(slots), _ptr(out_bar), *(_ptr(t) for t in outs), _ptr(scratch),
-                                        scratch.numel(), _stream_handle(None))
+                                        scratch.numel(), torch._C._cuda_getCurrentRawStream(X.get_device()))
     _check(st, "more_experts_backward")
     return outs
 
@@ -485,7 +486,7 @@ def moe_layer(X: torch.Tensor, R1: torch.Tensor, R2: torch.Tensor, W_up: torch.T
         out = _output(out, "out", torch.bfloat16, (N, h), X.device)
         scratch = _scratch(scratch, moe_layer_scratch_bytes(N, h, s, M, k), X.device)
         st = _lib.more_moe_layer(_ptr(X), _ptr(R1), _ptr(R2), _ptr(W_up), _ptr(W_down), N, h, r, s, M, k, _ptr(out),
-                                 _ptr(scratch), scratch.numel(), _stream_handle(None))
+                                 _ptr(scratch), scratch.numel(), torch._C._cuda_getCurrentRawStream(X.get_device()))
     _check(st, "more_moe_layer")
     return out
 
@@ -504,7 +505,7 @@ def moe_layer_int8(X: torch.Tensor, R1: torch.Tensor, R2: torch.Tensor, W_up: to
         scratch = _scratch(scratch, moe_layer_int8_scratch_bytes(N, h, s, M, k), X.device)
         st = _lib.more_moe_layer_int8(_ptr(X), _ptr(R1), _ptr(R2), _ptr(W_up), _ptr(up_scale), _ptr(W_down),
                                       _ptr(down_scale), N, h, r, s, M, k, _ptr(out), _ptr(scratch), scratch.numel(),
-                                      _stream_handle(None))
+                                      torch._C._cuda_getCurrentRawStream(X.get_device()))
     _check(st, "more_moe_layer_int8")
     return out
 

@@ -44,7 +44,6 @@ constexpr int kSlots = 4;                   // batches of a warp's ring
 constexpr uint32_t kRing = 128 * 1024;      // all warps' rings
 constexpr uint32_t kSmemMost = 200 * 1024;  // dynamic
 constexpr int kCandidates = 512;  // as many as threads: where there is no bound there may be that many logits
-constexpr int kHeld = 8;  // keys that a thread keeps in registers while a token's experts are chosen
 
 struct LayerArgs {
   const __nv_bfloat16 *X, *R1, *R2;
@@ -270,124 +269,107 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
-__device__ void select_experts(const LayerArgs& a, int n, Select& s, int32_t* idx, float* gate) {
-  const float* l = a.logits + (size_t)n * a.M;
-  uint32_t top = 0;  // below every number's key; a NaN logit is never chosen
-  uint32_t held[kHeld];  // this thread's first keys
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const int e = threadIdx.x + i * kThreads;
-    const float v = e < a.M ? l[e] : NAN;
-    held[i] = v == v ? key_of(v) : 0;
-  }
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) top = max(top, held[i]);
-#pragma unroll 4
-  for (int e = threadIdx.x + kHeld * kThreads; e < a.M; e += kThreads) {
-    const float v = l[e];
-    top = max(top, v == v ? key_of(v) : 0);
-  }
-  const uint32_t warp_top = __reduce_max_sync(0xffffffffu, top);
-  if ((threadIdx.x & 31) == 0) s.top[threadIdx.x >> 5] = warp_top;
+// Logits at or above `bound` (equal ones: of experts below `limit`) as candidates; their number.
+__device__ __forceinline__ int collect(const float* l, int M, uint32_t bound, int limit, bool any, Select& s) {
+  if (threadIdx.x == 0) s.count = 0;
   __syncthreads();
-  uint32_t bound = 0;
-  if (a.k <= kWarps) {
-    const int lane = threadIdx.x & 31;
-    const uint32_t mine = lane < kWarps ? s.top[lane] : 0;
-    int rank = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const uint32_t o = s.top[w];
-      rank += o > mine || (o == mine && w < lane);
-    }
-    const unsigned at = __ballot_sync(0xffffffffu, lane < kWarps && rank == a.k - 1);
-    bound = __shfl_sync(0xffffffffu, mine, __ffs(at) - 1);
-  }
-  int limit = 0x7fffffff;  // candidates at the bound itself: only experts below this
-  auto collect = [&]() {
-    if (threadIdx.x == 0) s.count = 0;
-    __syncthreads();
-    auto take = [&](uint32_t key, int e) {
-      if (key != 0 && key >= bound && (key > bound || e < limit)) {
+  if (any) {
+#pragma unroll 1
+    for (int e = threadIdx.x; e < M; e += kThreads) {
+      const float v = l[e];
+      const uint32_t key = key_of(v);
+      if (v == v && key >= bound && (key > bound || e < limit)) {
         const int at = atomicAdd(&s.count, 1);
         if (at < kCandidates) {
           s.key[at] = key;
           s.expert[at] = e;
         }
       }
-    };
-    if (top >= bound) {
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) take(held[i], threadIdx.x + i * kThreads);
-#pragma unroll 1
-      for (int e = threadIdx.x + kHeld * kThreads; e < a.M; e += kThreads) {
-        const float v = l[e];
-        take(v == v ? key_of(v) : 0, e);
-      }
-    }
-    __syncthreads();
-    return s.count;
-  };
-  int count = collect();
-  if (count > kCandidates) {
-    uint32_t lo = bound, hi = 0xffffffffu;  // the largest lo with at least k keys at or above it: the k-th largest key
-    while (lo < hi) {
-      const uint32_t mid = lo + (hi - lo) / 2 + 1;
-      int c = 0;
-      for (int e = threadIdx.x; e < a.M; e += kThreads) {
-        const float v = l[e];
-        c += v == v && key_of(v) >= mid;
-      }
-      int total = 0;  // a thread counts as many as it has, up to k
-      for (int j = 0; j < a.k; ++j) total += __syncthreads_count(c > j);
-      if (total >= a.k)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    bound = lo;
-    int from = 0, to = a.M;  // the fewest first experts [0, to) whose ties, with the larger keys, make k
-    while (from < to) {
-      const int half = (from + to) / 2;
-      int c = 0;
-      for (int e = threadIdx.x; e < a.M; e += kThreads) {
-        const float v = l[e];
-        const uint32_t key = key_of(v);
-        c += v == v && (key > bound || (key == bound && e < half));
-      }
-      int total = 0;
-      for (int j = 0; j < a.k; ++j) total += __syncthreads_count(c > j);
-      if (total >= a.k)
-        to = half;
-      else
-        from = half + 1;
-    }
-    limit = to;
-    count = collect();
-  }
-  // ranks
-  for (int c = threadIdx.x; c < count; c += kThreads) {
-    const uint32_t key = s.key[c];
-    const int e = s.expert[c];
-    int rank = 0;
-#pragma unroll 4
-    for (int o = 0; o < count; ++o) rank += s.key[o] > key || (s.key[o] == key && s.expert[o] < e);
-    if (rank < a.k) {
-      s.value[rank] = value_of(key);
-      idx[n * a.k + rank] = e;
     }
   }
   __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
+  return s.count;
+}
+
+// Too many candidates: the k-th largest key by bisection, and of its ties the first experts that make k.
+__device__ __noinline__ int collect_exactly(const float* l, int M, int k, uint32_t bound, Select& s) {
+  uint32_t lo = bound, hi = 0xffffffffu;
+  while (lo < hi) {
+    const uint32_t mid = lo + (hi - lo) / 2 + 1;
+    int c = 0;
+    for (int e = threadIdx.x; e < M; e += kThreads) {
+      const float v = l[e];
+      c += v == v && key_of(v) >= mid;
+    }
+    int total = 0;  // a thread counts as many as it has, up to k
+    for (int j = 0; j < k; ++j) total += __syncthreads_count(c > j);
+    if (total >= k)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  int from = 0, to = M;
+  while (from < to) {
+    const int half = (from + to) / 2;
+    int c = 0;
+    for (int e = threadIdx.x; e < M; e += kThreads) {
+      const float v = l[e];
+      const uint32_t key = key_of(v);
+      c += v == v && (key > lo || (key == lo && e < half));
+    }
+    int total = 0;
+    for (int j = 0; j < k; ++j) total += __syncthreads_count(c > j);
+    if (total >= k)
+      to = half;
+    else
+      from = half + 1;
+  }
+  return collect(l, M, lo, to, true, s);
+}
+
+__device__ void select_experts(const LayerArgs& a, int n, Select& s, int32_t* idx, float* gate) {
+  const float* l = a.logits + (size_t)n * a.M;
+  const int lane = threadIdx.x & 31;
+  uint32_t top = 0;  // below every number's key; a NaN logit is never chosen
+#pragma unroll 8
+  for (int e = threadIdx.x; e < a.M; e += kThreads) {
+    const float v = l[e];
+    top = max(top, v == v ? key_of(v) : 0);
+  }
+  const uint32_t warp_top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) s.top[threadIdx.x >> 5] = warp_top;
+  __syncthreads();
+  const uint32_t mine = lane < kWarps ? s.top[lane] : 0;
+  int rank = 0;
+#pragma unroll 4
+  for (int w = 0; w < kWarps; ++w) {
+    const uint32_t o = s.top[w];
+    rank += o > mine || (o == mine && w < lane);
+  }
+  const unsigned at = __ballot_sync(0xffffffffu, lane < kWarps && rank == a.k - 1);  // k <= 16 warps
+  const uint32_t bound = __shfl_sync(0xffffffffu, mine, __ffs(at) - 1);
+  int count = collect(l, a.M, bound, 0x7fffffff, top >= bound, s);
+  if (count > kCandidates) count = collect_exactly(l, a.M, a.k, bound, s);
+  for (int c = threadIdx.x; c < count; c += kThreads) {
+    const uint32_t key = s.key[c];
+    const int e = s.expert[c];
+    int r = 0;
+#pragma unroll 4
+    for (int o = 0; o < count; ++o) r += s.key[o] > key || (s.key[o] == key && s.expert[o] < e);
+    if (r < a.k) {
+      s.value[r] = value_of(key);
+      idx[n * a.k + r] = e;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < 16) {
     const bool in = lane < a.k && lane < count;
-    const float top_v = s.value[0];
-    const float ex = in ? expf(s.value[lane] - top_v) : 0.f;
+    const float ex = in ? expf(s.value[lane] - s.value[0]) : 0.f;
     float sum = ex;
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d, 16);
+    for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffu, sum, d, 16);
     if (lane < a.k) {
-      gate[n * a.k + lane] = in ? ex / sum : 0.f;
+      gate[n * a.k + lane] = in ? __fdividef(ex, sum) : 0.f;
       if (!in) idx[n * a.k + lane] = -1;  // fewer than k numbers among the logits
     }
   }
@@ -919,7 +901,7 @@ __device__ __forceinline__ void down_phase(const LayerArgs& a, const Shared& sh,
 }
 
 template <bool I8>
-__global__ void __launch_bounds__(kThreads, 1) layer_kernel(const LayerArgs a, int rows_each) {
+__global__ void __launch_bounds__(kThreads, 1) layer_kernel(const __grid_constant__ LayerArgs a, int rows_each) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ union {
     float part[kWarps][16];
