@@ -228,7 +228,7 @@ __device__ __forceinline__ uint2 round8x8(uint4 w, float div, float inv) {
 
 // One warp per row (width a multiple of 16): no barrier, and enough rows in flight to cover the latency of one.  The
 // first 2048 values stay in registers between finding the largest and rounding; what is beyond is read again.
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, 8)
     quantize_bf16_kernel(const __nv_bfloat16* __restrict__ v, int64_t rows, int width, int8_t* __restrict__ q,
                          float* __restrict__ scale) {
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);

@@ -186,10 +186,19 @@ struct Ring {
   }
 };
 
+// The wait for a free stage polls first: the hardware wakes a suspended thread so late that the loads fall behind (first
+// product at h = 2048, s = 64: 448 us with suspended waits, 388 us so; polling in the MMA thread's waits as well: 393 us).
+__device__ __forceinline__ bool poll_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          unsigned int* status) {
+  for (int i = 0; i < 4000; ++i)
+    if (mbar_test_wait(bar, parity)) return true;
+  return bounded_wait(bar, parity, abort_flag, status);
+}
+
 template <class S>
 __device__ __forceinline__ bool wait_empty(const Ring& r, const Bars& b, int lane, unsigned int* status) {
   int ok = 1;
-  if (lane == 0) ok = bounded_wait(&b.empty[r.pos.i], r.pos.phase ^ 1u, b.abort_flag, status);
+  if (lane == 0) ok = poll_wait(&b.empty[r.pos.i], r.pos.phase ^ 1u, b.abort_flag, status);
   return __shfl_sync(0xffffffffu, ok, 0);
 }
 
@@ -487,11 +496,18 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// int32 to fp32.  `small`: every |v| < 2^22, where the value drops into a float's mantissa with full-rate
+// int32 to fp32, in place.  `small`: every |v| < 2^22, where the value drops into a float's mantissa with full-rate
 // instructions; conversions run at an eighth of that rate, and a second product of 64 values a row is one MMA step of
 // work for 256 columns of conversions.
-__device__ __forceinline__ float from_int(uint32_t v, bool small) {
-  return small ? __uint_as_float(v + 0x4b400000u) - 12582912.f : (float)(int)v;
+template <int N>
+__device__ __forceinline__ void from_int(uint32_t* v, bool small) {
+  if (small) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __float_as_uint(__uint_as_float(v[i] + 0x4b400000u) - 12582912.f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __float_as_uint((float)(int)v[i]);
+  }
 }
 
 __device__ __forceinline__ float sigmoid(float a) { return __fdividef(1.f, 1.f + expf(-a)); }
@@ -610,6 +626,8 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
       tmem_wait_ld();
       reg_fence<32>(va);
       reg_fence<32>(vb);
+      from_int<32>(va, small);
+      from_int<32>(vb, small);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) release<PAIR>(&b.acc_empty[d.i]);
@@ -618,8 +636,8 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
       const int width = min(32, p.s - hh * 32);  // of this half: 32, 16 or none
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const float a = from_int(va[i], small) * (row_factor * scale_at(scales, i, sa));
-        const float u = from_int(vb[i], small) * (row_factor * scale_at(scales + HALF / 2 * 4, i, sb));
+        const float a = __uint_as_float(va[i]) * (row_factor * scale_at(scales, i, sa));
+        const float u = __uint_as_float(vb[i]) * (row_factor * scale_at(scales + HALF / 2 * 4, i, sb));
         const float m = a * sigmoid(a) * u;
         va[i] = __float_as_uint(m);
         if (i < width) top = fmaxf(top, fabsf(m));
@@ -656,6 +674,10 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
         tmem_wait_ld();
         reg_fence<32>(va);
         reg_fence<32>(vb);
+        if constexpr (S::kEight) {
+          from_int<32>(va, small);
+          from_int<32>(vb, small);
+        }
         if (c + 32 >= HALF / 2) {
           tc_fence_before();
           __syncwarp();
@@ -671,8 +693,8 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
           for (int i = 0; i < 8; ++i) {
             float a, u;
             if constexpr (S::kEight) {
-              a = from_int(va[q + i], small) * (row_factor * scale_at(scales + (c + q) * 4, i, sa));
-              u = from_int(vb[q + i], small) * (row_factor * scale_at(scales + (HALF / 2 + c + q) * 4, i, sb));
+              a = __uint_as_float(va[q + i]) * (row_factor * scale_at(scales + (c + q) * 4, i, sa));
+              u = __uint_as_float(vb[q + i]) * (row_factor * scale_at(scales + (HALF / 2 + c + q) * 4, i, sb));
             } else {
               a = __uint_as_float(va[q + i]);
               u = __uint_as_float(vb[q + i]);
@@ -752,6 +774,13 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
             tmem_ld_x32(acc + c + 32, v + 32);
             tmem_wait_ld();
             reg_fence<64>(v);
+            if constexpr (S::kEight) {  // all the scales before the first store to shared memory: the reads overlap
+              from_int<64>(v, small);
+              float4 sc;
+#pragma unroll
+              for (int i = 0; i < 64; ++i)
+                v[i] = __float_as_uint(__uint_as_float(v[i]) * (row_factor * scale_at(scales + c / 128 * 256, i, sc)));
+            }
           }
           if (last && !empty) {
             tc_fence_before();
@@ -765,15 +794,8 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             float f[8];
-            float4 sc;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if constexpr (MODE == kDown8) {
-                f[i] = from_int(v[q * 8 + i], small) * (row_factor * scale_at(scales + (c / 128 * 64 + q * 8) * 4, i, sc));
-              } else {
-                f[i] = __uint_as_float(v[q * 8 + i]) * row_factor;
-              }
-            }
+            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[q * 8 + i]) * (S::kEight ? 1.f : row_factor);
             st_shared_v4(stage + lane * 128 + ((q ^ (lane & 7)) << 4),
                          make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])));
           }
