@@ -102,7 +102,9 @@ __device__ __forceinline__ int8_t round8(float v, float top, float inv) {
 }
 
 // Lays the rows out from offsets, slots and gates (experts_rows.cu).
-cudaError_t launch_rows(const ExpertsArgs& a, const Rows& r, int tile_rows);
+// With token_scale also each row's scale.
+cudaError_t launch_rows(const ExpertsArgs& a, const Rows& r, int tile_rows, const float* token_scale = nullptr,
+                        float* row_scale = nullptr);
 // Rows of `pitch` bytes (a multiple of 16) picked by token into the padded layout.
 cudaError_t launch_pick(const ExpertsArgs& a, const Rows& r, const void* src, int pitch, void* dst);
 // out[n] = sum over j of y[slot_row[n k + j]], fp32 sums in the order of j, rounded once to bf16.

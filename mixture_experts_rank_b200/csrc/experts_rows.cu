@@ -94,7 +94,8 @@ __global__ void __launch_bounds__(kScanThreads)
 // One CTA per tile, a thread per row: the rows' slots, tokens and gates, and each slot's row.
 __global__ void __launch_bounds__(2 * kTileRows)
     rows_fill_kernel(const int32_t* __restrict__ offsets, const int32_t* __restrict__ slots,
-                     const float* __restrict__ gate, int64_t S, int k, Rows out, unsigned int* status) {
+                     const float* __restrict__ gate, int64_t S, int k, const float* __restrict__ token_scale,
+                     float* __restrict__ row_scale, Rows out, unsigned int* status) {
   if ((int)blockIdx.x >= *out.n_tiles) return;
   const int4 t = out.tiles[blockIdx.x];
   const int r = threadIdx.x;
@@ -106,7 +107,9 @@ __global__ void __launch_bounds__(2 * kTileRows)
   const bool real = ok && r < t.z;
   const int row = t.y + r;
   out.row_slot[row] = real ? slot : -1;
-  out.row_token[row] = ok ? slot / k : 0;
+  const int token = ok ? slot / k : 0;
+  out.row_token[row] = token;
+  if (token_scale) row_scale[row] = token_scale[token];
   out.row_gate[row] = real ? gate[slot] : 0.f;
   if (real) out.slot_row[slot] = row;
 }
@@ -310,13 +313,14 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
-cudaError_t launch_rows(const ExpertsArgs& a, const Rows& r, int tile_rows) {
+cudaError_t launch_rows(const ExpertsArgs& a, const Rows& r, int tile_rows, const float* token_scale,
+                        float* row_scale) {
   const int64_t S = a.S();
   cudaError_t e = cudaMemsetAsync(r.slot_row, 0xff, sizeof(int32_t) * (size_t)S, a.stream);
   if (e != cudaSuccess) return e;
   rows_scan_kernel<<<1, kScanThreads, 0, a.stream>>>(a.offsets, S, a.M, tile_rows, r, a.status);
-  rows_fill_kernel<<<(unsigned)max_tiles(S, a.M, tile_rows), tile_rows, 0, a.stream>>>(a.offsets, a.slots, a.gate, S,
-                                                                                        a.k, r, a.status);
+  rows_fill_kernel<<<(unsigned)max_tiles(S, a.M, tile_rows), tile_rows, 0, a.stream>>>(
+      a.offsets, a.slots, a.gate, S, a.k, token_scale, row_scale, r, a.status);
   return cudaGetLastError();
 }
 

@@ -50,7 +50,7 @@ struct Shape {
   static constexpr bool kIsDown = MODE == kDown || MODE == kDown8;
   static constexpr bool kIsDw = MODE == kDwUp || MODE == kDwDown;
   static constexpr bool kGathers = !PAIR && (kIsUp || kIsDw || MODE == kBack);  // one operand is picked by token
-  static constexpr int kThreads = PAIR ? 12 * 32 : 14 * 32;
+  static constexpr int kThreads = kGathers ? 14 * 32 : 12 * 32;
   static constexpr int kRows = PAIR ? 2 * kTileRows : kTileRows;  // rows (or channels) of a tile
   static constexpr bool kStaged = kIsDown || MODE == kDx || kIsDw;  // epilogue goes through shared memory
   // columns of one accumulator, and its place in TMEM
@@ -86,7 +86,7 @@ struct Params {
   void* out;      // kUp: H; kUp8: H in fp32, or in 8 bits with out_scale; kDown, kDx: rows of h; kBack: [da, db]
   __nv_bfloat16* out2;  // kBack: gate * m
   float* part;          // kBack: the gate's gradient, a partial sum per HALF / 2 columns
-  const float* row_scale;  // kUp8: by token; kDown8: by row
+  const float* row_scale;  // 8 bits: the rows' scales
   const float* col_scale;
   unsigned int* status;
 };
@@ -526,7 +526,7 @@ template <int MODE, int HALF, bool PAIR>
 struct Info {
   static constexpr int kOwn = MODE == kUp8 ? HALF / 2 : 64;  // columns of a part: A's and B's, or the two chunks'
   static constexpr int kScaleRegs = Shape<MODE, HALF, PAIR>::kEight ? 2 * kOwn / 32 : 0;
-  float factor = 1.f;
+  float factor = 1.f, factor2 = 1.f;  // multiplied when they are used: here that would wait for them
   int slot = -1;
   float scale[kScaleRegs ? kScaleRegs : 1];
 };
@@ -540,8 +540,8 @@ __device__ __forceinline__ Info<MODE, HALF, PAIR> row_info(const Params& p, cons
     const bool in = t < k.padded;
     const int row = k.row + t;
     if constexpr (S::kIsDown || MODE == kBack) r.factor = in ? p.rows.row_gate[row] : 0.f;
-    if constexpr (MODE == kDown8) r.factor *= t < k.n ? p.row_scale[row] : 0.f;
-    if constexpr (MODE == kUp8) r.factor = in ? p.row_scale[p.rows.row_token[row]] : 0.f;
+    if constexpr (MODE == kDown8) r.factor2 = t < k.n ? p.row_scale[row] : 0.f;
+    if constexpr (MODE == kUp8) r.factor = in ? p.row_scale[row] : 0.f;
     if constexpr (MODE == kBack) r.slot = in ? p.rows.row_slot[row] : -1;
   }
 #pragma unroll
@@ -597,7 +597,7 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
     const bool empty = S::kIsDw && k.padded == 0;
     const int row = k.row + t;
     if (at.w == at.first()) info = row_info<MODE, HALF, PAIR>(p, k, t, lane, hh);
-    const float row_factor = info.factor;
+    const float row_factor = info.factor * info.factor2;
     const int slot = info.slot;
     if constexpr (S::kEight) {
       __syncwarp();
@@ -776,10 +776,21 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
             reg_fence<64>(v);
             if constexpr (S::kEight) {  // all the scales before the first store to shared memory: the reads overlap
               from_int<64>(v, small);
-              float4 sc;
+              uint4 sc[8];
 #pragma unroll
-              for (int i = 0; i < 64; ++i)
-                v[i] = __float_as_uint(__uint_as_float(v[i]) * (row_factor * scale_at(scales + c / 128 * 256, i, sc)));
+              for (int half = 0; half < 64; half += 32) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sc[i] = ld_shared_v4(scales + c / 128 * 256 + half * 4 + i * 16);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const uint32_t four[4] = {sc[i].x, sc[i].y, sc[i].z, sc[i].w};
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    uint32_t& x = v[half + 4 * i + j];
+                    x = __float_as_uint(__uint_as_float(x) * (row_factor * __uint_as_float(four[j])));
+                  }
+                }
+              }
             }
           }
           if (last && !empty) {
@@ -977,7 +988,7 @@ int tiles_of(int n, int bn) { return (n + bn - 1) / bn; }
 
 // H = silu(X A^T) * (X B^T).  pair: X holds the rows already picked, [R][h].
 template <int MODE>
-cudaError_t run_up(const ExpertsArgs& a, const Rows& rows, const void* X, const float* x_scale, void* H,
+cudaError_t run_up(const ExpertsArgs& a, const Rows& rows, const void* X, const float* row_scale, void* H,
                    float* h_scale, bool pair) {
   constexpr int bytes = MODE == kUp8 ? 1 : 2, box = 128 / bytes;
   Params p = {};
@@ -987,7 +998,7 @@ cudaError_t run_up(const ExpertsArgs& a, const Rows& rows, const void* X, const 
   p.h = a.h;
   p.cols = a.s;
   p.out = H;
-  p.row_scale = x_scale;
+  p.row_scale = row_scale;
   p.out_scale = h_scale;
   p.col_scale = a.up_scale;
   p.X = X;
@@ -1035,7 +1046,7 @@ struct Buffers {
   Rows rows;
   void *H, *Hq, *Xq, *Y;
   void *Xr, *Dr;  // X's (or its 8 bits') and y_bar's rows in the padded layout, for CTA pairs
-  float *x_scale, *h_scale, *part;
+  float *x_scale, *row_scale, *h_scale, *part;
   __nv_bfloat16 *pre, *mid;
   size_t bytes;
 };
@@ -1060,6 +1071,7 @@ Buffers carve(void* scratch, int64_t N, int h, int s, int M, int k, int kind) {
   } else if (kind == kInt8) {
     b.Xq = c.take<int8_t>(N * h);
     b.x_scale = c.take<float>(N);
+    b.row_scale = c.take<float>(R);
     if (pair) b.Xr = c.take<int8_t>(R * h);
     if (s > 64) b.H = c.take<float>(R * s);
     b.Hq = c.take<int8_t>(R * s);
@@ -1097,14 +1109,14 @@ cudaError_t launch_experts(const ExpertsArgs& a) {
 cudaError_t launch_experts_int8(const ExpertsArgs& a) {
   const Buffers b = carve(a.scratch, a.N, a.h, a.s, a.M, a.k, kInt8);
   const bool pair = takes_pairs(a.S(), a.s, a.M);
-  MORE_TRY(launch_rows(a, b.rows, pair ? 2 * kTileRows : kTileRows));
   MORE_TRY(launch_quantize_bf16(static_cast<const __nv_bfloat16*>(a.X), a.N, a.h, static_cast<int8_t*>(b.Xq),
                                 b.x_scale, a.stream));
+  MORE_TRY(launch_rows(a, b.rows, pair ? 2 * kTileRows : kTileRows, b.x_scale, b.row_scale));
   if (pair) MORE_TRY(launch_pick(a, b.rows, b.Xq, a.h, b.Xr));
   if (a.s <= 64) {  // one tile holds the middle of an expert's rows: rounded to 8 bits in the product's epilogue
-    MORE_TRY(run_up<kUp8>(a, b.rows, b.Xq, b.x_scale, b.Hq, b.h_scale, false));
+    MORE_TRY(run_up<kUp8>(a, b.rows, b.Xq, b.row_scale, b.Hq, b.h_scale, false));
   } else {
-    MORE_TRY(run_up<kUp8>(a, b.rows, pair ? b.Xr : b.Xq, b.x_scale, b.H, nullptr, pair));
+    MORE_TRY(run_up<kUp8>(a, b.rows, pair ? b.Xr : b.Xq, b.row_scale, b.H, nullptr, pair));
     MORE_TRY(launch_quantize_rows(a, b.rows, static_cast<const float*>(b.H), a.s, static_cast<int8_t*>(b.Hq),
                                   b.h_scale, pair ? 2 * kTileRows : kTileRows));
   }
