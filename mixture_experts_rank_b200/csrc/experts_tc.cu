@@ -42,6 +42,7 @@ constexpr uint32_t kBox = 64 * 128;            // 8 KB: a box of 64 rows x 128 b
 constexpr uint32_t kStageOut = 32 * 128;       // a warp's staging: 32 rows x 64 bf16 columns
 constexpr int kScales = 128;  // column scales that a warp needs of a tile
 constexpr int kMaxStages = 6;
+constexpr int kRun = 1024;  // of K, between additions in registers
 
 template <int MODE, int HALF, bool PAIR>
 struct Shape {
@@ -53,6 +54,10 @@ struct Shape {
   static constexpr int kThreads = kGathers ? 14 * 32 : 12 * 32;
   static constexpr int kRows = PAIR ? 2 * kTileRows : kTileRows;  // rows (or channels) of a tile
   static constexpr bool kStaged = kIsDown || MODE == kDx || kIsDw;  // epilogue goes through shared memory
+  // The tensor cores cut sums off, they do not round them: a sum over K comes out too small by about 1e-9 K of itself, and
+  // the gate's gradient, which is fp32 to the end, by three times that.  Tiles of 3 x 64 columns therefore take their
+  // products in runs of kRun, added in registers; 3 x 128 columns are more than the registers hold.
+  static constexpr bool kRuns = MODE == kBack && HALF == 64;
   // columns of one accumulator, and its place in TMEM
   static constexpr int kCols = kIsUp ? 2 * HALF : MODE == kBack ? 3 * HALF : 256;
   static constexpr int kAccStride = kCols <= 128 ? 128 : 256;
@@ -447,40 +452,59 @@ __device__ void mma_role(const Params& p, const Bars& b, uint8_t* smem, uint32_t
   for (Cursor<S, PAIR> at(p); !at.done(); at.next(p)) {
     const Work k = at.cur;
     if (S::kIsDw && k.padded == 0) continue;  // the epilogue writes zeros
-    if (!bounded_wait(&b.acc_empty[d.i], d.phase ^ 1u, b.abort_flag, p.status)) goto done;
-    tc_fence_after();
-    {
-      const uint32_t acc = tmem + d.i * S::kAccStride;
-      const int len1 = S::kIsDw ? k.padded : p.k1;
-      // columns of this tile's product: all, or up to the last of the weights' gradient, whole MMA steps
-      const int n = MODE == kDwDown && !PAIR ? min(256, (p.cols - k.c0 + 15) & ~15) : S::kIsUp || MODE == kBack ? 2 * HALF : 256;
-      const uint32_t idesc = S::kEight ? idesc_s8_s32(S::kRows, n) : idesc_bf16_f32(S::kRows, n, kAMn, kBMn);
-      for (int x = 0; x < len1; x += S::kKBlock) {
+    const int len1 = S::kIsDw ? k.padded : p.k1;
+    // columns of this tile's product: all, or up to the last of the weights' gradient, whole MMA steps
+    const int n = MODE == kDwDown && !PAIR ? min(256, (p.cols - k.c0 + 15) & ~15) : S::kIsUp || MODE == kBack ? 2 * HALF : 256;
+    const uint32_t idesc = S::kEight ? idesc_s8_s32(S::kRows, n) : idesc_bf16_f32(S::kRows, n, kAMn, kBMn);
+    uint32_t acc = 0;
+    for (int x = 0; x < len1; x += S::kKBlock) {
+      const bool first = S::kRuns ? x % kRun == 0 : x == 0;
+      if (first) {
+        if (!bounded_wait(&b.acc_empty[d.i], d.phase ^ 1u, b.abort_flag, p.status)) goto done;
+        tc_fence_after();
+        acc = tmem + d.i * S::kAccStride;
+      }
+      if (!bounded_wait(&b.full[s.i], s.phase, b.abort_flag, p.status)) goto done;
+      if constexpr (S::kGathers) fence_proxy_async_smem();
+      tc_fence_after();
+      const uint64_t off = (uint32_t)s.i * (S::kStage >> 4);
+      stage_products<S::kEight, kAMn, kBMn, kMax, PAIR>(acc, a0 + off, b0 + off, idesc,
+                                                        (len1 - x + S::kKStep - 1) / S::kKStep, first);
+      done_with<PAIR>(&b.empty[s.i]);
+      s.next(S::kStages);
+      if (S::kRuns && ((x + S::kKBlock) % kRun == 0 || x + S::kKBlock >= len1)) {
+        done_with<PAIR>(&b.acc_full[d.i]);
+        d.next(S::kAccs);
+      }
+    }
+    if constexpr (MODE == kBack) {
+      const uint64_t b1 = smem_desc(st0 + kABytes, kBox, 1024, kSwizzle128B);
+      for (int x = 0; x < p.k2; x += S::kKBlock) {
+        const bool first = S::kRuns ? x % kRun == 0 : x == 0;
+        if (S::kRuns && first) {
+          if (!bounded_wait(&b.acc_empty[d.i], d.phase ^ 1u, b.abort_flag, p.status)) goto done;
+          tc_fence_after();
+          acc = tmem + d.i * S::kAccStride;
+        }
         if (!bounded_wait(&b.full[s.i], s.phase, b.abort_flag, p.status)) goto done;
         if constexpr (S::kGathers) fence_proxy_async_smem();
         tc_fence_after();
         const uint64_t off = (uint32_t)s.i * (S::kStage >> 4);
-        stage_products<S::kEight, kAMn, kBMn, kMax, PAIR>(acc, a0 + off, b0 + off, idesc,
-                                                    (len1 - x + S::kKStep - 1) / S::kKStep, x == 0);
+        stage_products<false, false, true, kMax, PAIR>(acc + 2 * HALF, a0 + off, b1 + off,
+                                                       idesc_bf16_f32(S::kRows, HALF, 0, 1),
+                                                       (p.k2 - x + S::kKStep - 1) / S::kKStep, first);
         done_with<PAIR>(&b.empty[s.i]);
         s.next(S::kStages);
-      }
-      if constexpr (MODE == kBack) {
-        const uint64_t b1 = smem_desc(st0 + kABytes, kBox, 1024, kSwizzle128B);
-        for (int x = 0; x < p.k2; x += S::kKBlock) {
-          if (!bounded_wait(&b.full[s.i], s.phase, b.abort_flag, p.status)) goto done;
-          if constexpr (S::kGathers) fence_proxy_async_smem();
-          tc_fence_after();
-          const uint64_t off = (uint32_t)s.i * (S::kStage >> 4);
-          stage_products<false, false, true, kMax, PAIR>(acc + 2 * HALF, a0 + off, b1 + off, idesc_bf16_f32(S::kRows, HALF, 0, 1),
-                                                   (p.k2 - x + S::kKStep - 1) / S::kKStep, x == 0);
-          done_with<PAIR>(&b.empty[s.i]);
-          s.next(S::kStages);
+        if (S::kRuns && ((x + S::kKBlock) % kRun == 0 || x + S::kKBlock >= p.k2)) {
+          done_with<PAIR>(&b.acc_full[d.i]);
+          d.next(S::kAccs);
         }
       }
     }
-    done_with<PAIR>(&b.acc_full[d.i]);
-    d.next(S::kAccs);
+    if constexpr (!S::kRuns) {
+      done_with<PAIR>(&b.acc_full[d.i]);
+      d.next(S::kAccs);
+    }
   }
 done:
   if constexpr (PAIR)
@@ -606,12 +630,12 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
       __syncwarp();
     }
     if (at.more()) info = row_info<MODE, HALF, PAIR>(p, PAIR ? part_of<S::kIsDw>(at.nxt, rank) : at.nxt, t, lane, hh);  // used a tile from now
-    if (!empty) {
+    if (!empty && !S::kRuns) {
       if (!bounded_wait(&b.acc_full[d.i], d.phase, b.abort_flag, p.status)) break;
       tc_fence_after();
     }
     const uint32_t acc = tmem + lanes + d.i * S::kAccStride;
-    if (!S::kIsDw && sp * 32 >= k.padded) {  // none of this warp's rows is in the tile
+    if (!S::kIsDw && !S::kRuns && sp * 32 >= k.padded) {  // none of this warp's rows is in the tile
       __syncwarp();
       if (lane == 0) release<PAIR>(&b.acc_empty[d.i]);
       d.next(S::kAccs);
@@ -713,21 +737,72 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
       }
     } else if constexpr (MODE == kBack) {
       float dot = 0.f;
+      float run_a[S::kRuns ? 32 : 1], run_b[S::kRuns ? 32 : 1], run_g[S::kRuns ? 32 : 1];
+      if constexpr (S::kRuns) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) run_a[i] = run_b[i] = run_g[i] = 0.f;
+        const int runs = (p.k1 + kRun - 1) / kRun;
+        bool ok = true;
+#pragma unroll 1
+        for (int r = 0; r < 2 * runs; ++r) {
+          if (!bounded_wait(&b.acc_full[d.i], d.phase, b.abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (sp * 32 < k.padded) {
+            const uint32_t from = tmem + lanes + d.i * S::kAccStride + hh * 32;
+            uint32_t v[32];
+            if (r < runs) {
+              tmem_ld_x32(from, v);
+              tmem_wait_ld();
+              reg_fence<32>(v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) run_a[i] += __uint_as_float(v[i]);
+              tmem_ld_x32(from + HALF, v);
+              tmem_wait_ld();
+              reg_fence<32>(v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) run_b[i] += __uint_as_float(v[i]);
+            } else {
+              tmem_ld_x32(from + 2 * HALF, v);
+              tmem_wait_ld();
+              reg_fence<32>(v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) run_g[i] += __uint_as_float(v[i]);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) release<PAIR>(&b.acc_empty[d.i]);
+          d.next(S::kAccs);
+        }
+        if (!ok) break;
+      }
 #pragma unroll 1
       for (int c = 0; c < HALF / 2; c += 32) {
         const int col = hh * (HALF / 2) + c;
         uint32_t va[32], vb[32], vg[32];
-        tmem_ld_x32(acc + col, va);
-        tmem_ld_x32(acc + HALF + col, vb);
-        tmem_ld_x32(acc + 2 * HALF + col, vg);
-        tmem_wait_ld();
-        reg_fence<32>(va);
-        reg_fence<32>(vb);
-        reg_fence<32>(vg);
-        if (c + 32 >= HALF / 2) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) release<PAIR>(&b.acc_empty[d.i]);
+        if constexpr (S::kRuns) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            va[i] = __float_as_uint(run_a[i]);
+            vb[i] = __float_as_uint(run_b[i]);
+            vg[i] = __float_as_uint(run_g[i]);
+          }
+        } else {
+          tmem_ld_x32(acc + col, va);
+          tmem_ld_x32(acc + HALF + col, vb);
+          tmem_ld_x32(acc + 2 * HALF + col, vg);
+          tmem_wait_ld();
+          reg_fence<32>(va);
+          reg_fence<32>(vb);
+          reg_fence<32>(vg);
+          if (c + 32 >= HALF / 2) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) release<PAIR>(&b.acc_empty[d.i]);
+          }
         }
         const int g0 = k.c0 + col;
         if (t >= k.padded) continue;
@@ -842,7 +917,7 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
         }
       }
     }
-    if (!empty) d.next(S::kAccs);
+    if (!empty && !S::kRuns) d.next(S::kAccs);
   }
   if constexpr (S::kIsDw) {
     if (lane == 0) bulk_wait_group<0>();
@@ -1053,7 +1128,10 @@ struct Buffers {
 
 enum Kind { kForward = 0, kInt8 = 1, kBackward = 2 };
 
-int gate_parts(int s) { return s <= 64 ? 2 : (s + 127) / 128 * 2; }
+// Tiles of the backward's first kernel: 3 x 128 columns, or 3 x 64 for experts that have no more, and where h is so long
+// that the products want runs (the gate's gradient is then off by 6e-6 of itself at most, as at h = 2048 in one run).
+int back_half(int h, int s) { return s <= 64 || h > 2 * kRun ? 64 : 128; }
+int gate_parts(int h, int s) { return 2 * tiles_of(s, back_half(h, s)); }
 
 // CTA pairs with 256-row tiles, the rows picked by token copied together first.  For wide experts with enough rows to
 // fill such tiles; narrow ones read each picked row once anyway, and are bound by memory.
@@ -1083,7 +1161,7 @@ Buffers carve(void* scratch, int64_t N, int h, int s, int M, int k, int kind) {
     }
     b.pre = c.take<__nv_bfloat16>(R * 2 * s);
     b.mid = c.take<__nv_bfloat16>(R * s);
-    b.part = c.take<float>(R * gate_parts(s));
+    b.part = c.take<float>(R * gate_parts(h, s));
   }
   b.Y = c.take<__nv_bfloat16>(R * h);
   b.bytes = c.used;
@@ -1130,7 +1208,9 @@ cudaError_t launch_experts_backward(const ExpertsArgs& a) {
   const bool pair = takes_pairs(S, a.s, a.M);
   const int rows = pair ? 2 * kTileRows : kTileRows;
   const int64_t tiles = max_tiles(S, a.M, rows);
-  MORE_TRY(launch_rows(a, b.rows, rows));
+  const int half = back_half(a.h, a.s);
+  const bool back_pair = pair && half == 128;
+  MORE_TRY(launch_rows(a, b.rows, back_pair ? 2 * kTileRows : kTileRows));
   if (pair) {
     MORE_TRY(launch_pick(a, b.rows, a.X, 2 * a.h, b.Xr));
     MORE_TRY(launch_pick(a, b.rows, a.out_bar, 2 * a.h, b.Dr));
@@ -1151,20 +1231,20 @@ cudaError_t launch_experts_backward(const ExpertsArgs& a) {
     q.out2 = b.mid;
     q.part = b.part;
     // 3 x 128 columns leave TMEM one accumulator, 3 x 64 two; the wide tile reads x and y_bar half as often
-    const int half = a.s <= 64 ? 64 : 128;
     q.nc = tiles_of(a.s, half);
     MORE_MAP(&m1, a.W_up, 2, a.h, 2 * (int64_t)a.s, a.M, 64, half);
     MORE_MAP(&m3, a.W_down, 2, a.s, a.h, a.M, 64, 64);
-    if (pair) {
+    if (back_pair) {
       MORE_MAP(&m0, b.Xr, 2, a.h, R, 0, 64, kTileRows);
       MORE_MAP(&m2, b.Dr, 2, a.h, R, 0, 64, kTileRows);
       MORE_TRY((launch<kBack, 128, true>(a, q, tiles * q.nc, m0, m1, m2, m3)));
     } else if (half == 64) {
-      MORE_TRY((launch<kBack, 64, false>(a, q, tiles * q.nc, m1, m1, m1, m3)));
+      MORE_TRY((launch<kBack, 64, false>(a, q, max_tiles(S, a.M) * q.nc, m1, m1, m1, m3)));
     } else {
-      MORE_TRY((launch<kBack, 128, false>(a, q, tiles * q.nc, m1, m1, m1, m3)));
+      MORE_TRY((launch<kBack, 128, false>(a, q, max_tiles(S, a.M) * q.nc, m1, m1, m1, m3)));
     }
   }
+  if (pair && !back_pair) MORE_TRY(launch_rows(a, b.rows, rows));  // the same rows in tiles of 256
   {
     Params q = p;
     q.k1 = 2 * a.s;
@@ -1206,7 +1286,7 @@ cudaError_t launch_experts_backward(const ExpertsArgs& a) {
       MORE_TRY((launch<kDwDown, 64, false>(a, q, q.items, m1, m1, m2, m1)));
     }
   }
-  MORE_TRY(launch_gate_grads(a, b.rows, b.part, gate_parts(a.s), R));
+  MORE_TRY(launch_gate_grads(a, b.rows, b.part, gate_parts(a.h, a.s), R));
   return launch_combine(a, b.rows, static_cast<const __nv_bfloat16*>(b.Y), a.out);
 }
 

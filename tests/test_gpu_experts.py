@@ -13,6 +13,7 @@ SIZES = [  # N, h, s, M, k
     (130, 520, 64, 40, 5), (1000, 256, 72, 24, 4), (129, 64, 264, 1, 1), (513, 320, 136, 3, 2), (700, 1096, 392, 8, 3),
     (64, 128, 64, 1000, 16),
     (260, 1024, 160, 1, 1), (1500, 264, 1032, 4, 2), (3000, 200, 136, 16, 3),  # wide experts with many rows: CTA pairs
+    (70, 4104, 56, 4, 2), (500, 2112, 136, 2, 1),  # h long enough for sums in runs
 ]
 SIZES_8 = [  # the same with h and s in whole 16s
     (1, 16, 16, 8, 1), (1, 64, 16, 8, 8), (2, 2048, 64, 64, 8), (37, 80, 48, 16, 3), (300, 144, 208, 8, 2),
