@@ -164,3 +164,216 @@ def test_moe_layer_int8(size):
     assert ok() and untouched()
     scales = {n: args[n] for n in ("up_scale", "down_scale")}
     ref.check(out, *layer_reference(args, k, N <= 64, **scales), "out")
+
+
+def masked(args, drop):
+    """The same routing with some selections dropped, as dispatch does with an index outside [0, M)."""
+    import mixture_experts_rank_b200 as more
+    N, k = args["gate"].shape
+    M = args["offsets"].numel() - 1
+    idx = torch.empty(N * k, dtype=torch.int32, device="cuda")
+    idx[args["slots"].long()] = torch.repeat_interleave(torch.arange(M, dtype=torch.int32, device="cuda"),
+                                                        args["offsets"].diff().long())
+    idx[drop] = M + 5
+    offsets, slots = more.dispatch(idx.view(N, k), M)
+    torch.cuda.synchronize()
+    assert more.device_status() != 0  # dispatch reports the index
+    return dict(args, offsets=offsets, slots=slots)
+
+
+@pytest.mark.parametrize("size", [(37, 72, 24, 16, 3), (700, 320, 136, 3, 2)], ids=str)
+def test_selections_that_nobody_lists(size):
+    import mixture_experts_rank_b200 as more
+    args, d = make(*size)
+    N, k = size[0], size[4]
+    args = masked(args, list(range(0, 2 * k)) + [5 * k + 1])  # tokens 0 and 1 keep nothing
+    out = more.experts(**args)
+    got = more.experts_backward(**args, out_bar=d)
+    assert ok()
+    ref.check(out, *ref.forward(**args), "out")
+    assert (out[:2] == 0).all() and (got[0][:2] == 0).all() and (got[3][:2] == 0).all()
+    want, bound = ref.backward(**args, out_bar=d)
+    for name, t in zip(want, got):
+        ref.check(t, want[name], bound[name], name)
+    eight = int8_of(make(N, 80, 32, size[3], k)[0])
+    eight = masked(eight, list(range(0, 2 * k)))
+    out = more.experts_int8(**eight)
+    assert ok() and (out[:2] == 0).all()
+    ref.check(out, *ref.forward(**eight), "out")
+
+
+def test_broken_offsets_and_slots_are_reported():
+    import mixture_experts_rank_b200 as more
+    args, d = make(50, 64, 16, 8, 2)
+    for bad in ([0, 120] + [100] * 7, [-1] + [100] * 8, [0, 60, 30, 60, 70, 80, 90, 95, 100]):
+        out, untouched = guarded((50, 64), torch.bfloat16)
+        more.experts(**dict(args, offsets=torch.tensor(bad, dtype=torch.int32, device="cuda")), out=out)
+        torch.cuda.synchronize()
+        assert more.device_status() != 0 and untouched() and (out == 0).all()
+    slots = args["slots"].clone()
+    slots[3], slots[40] = 100, -7
+    lost = args["slots"][[3, 40]].long()
+    gate = args["gate"].clone()
+    gate.view(-1)[lost] = 0  # what a skipped selection comes to
+    out = more.experts(**dict(args, slots=slots))
+    got = more.experts_backward(**dict(args, slots=slots), out_bar=d)
+    torch.cuda.synchronize()
+    assert more.device_status() != 0
+    ref.check(out, *ref.forward(**dict(args, gate=gate)), "out")
+    want, bound = ref.backward(**dict(args, gate=gate), out_bar=d)
+    for i, name in enumerate(("X_bar", "W_up_bar", "W_down_bar")):
+        ref.check(got[i], want[name], bound[name], name)
+    assert (got[3].view(-1)[lost] == 0).all()
+
+
+def test_not_a_number_stays_with_its_token():
+    import mixture_experts_rank_b200 as more
+    args, _ = make(200, 128, 40, 8, 2)
+    clean = more.experts(**args)
+    X = args["X"].clone()
+    X[17, 3], X[90, 5] = float("nan"), float("inf")
+    out = more.experts(**dict(args, X=X))
+    assert ok()
+    keep = torch.ones(200, dtype=torch.bool, device="cuda")
+    keep[[17, 90]] = False
+    assert torch.equal(out[keep], clean[keep]) and not torch.isfinite(out[~keep]).all(1).any()
+    a = layer_inputs(9, 128, 16, 32, 16)
+    clean = more.moe_layer(**a, k=3)
+    X = a["X"].clone()
+    X[4, 7] = float("nan")  # no logit of it is a number: it selects nothing
+    out = more.moe_layer(**dict(a, X=X), k=3)
+    torch.cuda.synchronize()
+    assert more.device_status() != 0
+    keep = torch.arange(9, device="cuda") != 4
+    assert torch.equal(out[keep], clean[keep]) and (out[4] == 0).all()
+
+
+@pytest.mark.parametrize("M,k", [(4096, 8), (600, 16), (16, 16)])
+def test_layer_with_equal_logits_takes_the_lowest_experts(M, k):
+    import mixture_experts_rank_b200 as more
+    a = layer_inputs(3, 64, 16, 16, M)
+    a["R2"] = a["R2"][:, :1].repeat(1, M).contiguous()
+    out = more.moe_layer(**a, k=k)
+    assert ok()
+    idx = torch.arange(k, device="cuda", dtype=torch.int32).repeat(3, 1)
+    offsets, slots = more.dispatch(idx, M)
+    gate = torch.full((3, k), 1 / k, device="cuda")
+    ref.check(out, *ref.forward(a["X"], a["W_up"], a["W_down"], gate, offsets, slots, fp32_rows=True), "out")
+    a["R2"][:, M // 2:] *= 2  # two values: for every token one half is ahead of the other
+    out = more.moe_layer(**a, k=k)
+    assert ok()
+    ref.check(out, *layer_reference(a, k, True), "out")
+
+
+def every_call(seed=0):
+    """(name, call with given outputs) of each entry point, on inputs of its own."""
+    import mixture_experts_rank_b200 as more
+    args, d = make(300, 136, 72, 8, 2, seed)
+    wide, dw = make(600, 320, 136, 3, 2, seed)
+    eight = int8_of(make(300, 144, 80, 8, 2, seed)[0])
+    few = layer_inputs(7, 144, 16, 48, 24, seed)
+    many = layer_inputs(90, 144, 16, 48, 24, seed)
+    return {"experts": lambda: more.experts(**args), "pairs": lambda: more.experts(**wide),
+            "int8": lambda: more.experts_int8(**eight), "backward": lambda: more.experts_backward(**args, out_bar=d),
+            "backward pairs": lambda: more.experts_backward(**wide, out_bar=dw),
+            "layer": lambda: more.moe_layer(**few, k=3), "layer many": lambda: more.moe_layer(**many, k=3),
+            "layer int8": lambda: more.moe_layer_int8(**int8_of(few), k=3), "rows": lambda: more.quantize_rows(args["X"][:, :128].contiguous())}
+
+
+def same(a, b):
+    a, b = (x if isinstance(x, tuple) else (x,) for x in (a, b))
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("name", list(["experts", "pairs", "int8", "backward", "backward pairs", "layer", "layer many",
+                                       "layer int8", "rows"]))
+def test_repeated_streamed_and_captured_calls_agree(name):
+    f, other = every_call()[name], every_call(1)[name]
+    first = f()
+    torch.cuda.synchronize()
+    assert same(first, f())
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    want = other()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s1):
+        a = [f() for _ in range(4)]
+    with torch.cuda.stream(s2):
+        b = [other() for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(same(x, first) for x in a) and all(same(x, want) for x in b)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got, again = f(), f()
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert same(got, first) and same(again, first) and ok()
+
+
+def test_stream_argument_and_given_scratch():
+    import mixture_experts_rank_b200 as more
+    args, d = make(64, 72, 24, 8, 2)
+    want = more.experts(**args)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    scratch = torch.full((more.experts_scratch_bytes(64, 72, 24, 8, 2),), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    out = more.experts(**args, scratch=scratch, stream=s)
+    s.synchronize()
+    assert torch.equal(out, want)
+    with pytest.raises(more.MoreError):
+        more.experts(**args, scratch=scratch[:-256])
+    with pytest.raises(ValueError):
+        more.experts(**dict(args, X=args["X"].t().contiguous().t()))
+    with pytest.raises(ValueError):
+        more.experts(**args, out=torch.empty(64, 80, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(TypeError):
+        more.experts(**args, out=torch.empty(64, 72, device="cuda"))
+
+
+def test_no_tokens():
+    import mixture_experts_rank_b200 as more
+    args, d = make(0, 64, 16, 8, 2)
+    assert more.experts(**args).shape == (0, 64)
+    got = more.experts_backward(**args, out_bar=d)
+    assert ok() and got[0].shape == (0, 64) and (got[1] == 0).all() and (got[2] == 0).all()
+    a = layer_inputs(0, 64, 16, 16, 8)
+    assert more.moe_layer(**a, k=2).shape == (0, 64)
+
+
+def test_a_training_step_through_the_router_and_the_experts():
+    """route_train, dispatch, experts, then the backward of both: the chain that a training step makes of them, each
+    gradient against the formulas in 64 bits for the step's own selections."""
+    import mixture_experts_rank_b200 as more
+    N, h, r, s, M, k = 200, 128, 32, 48, 64, 4
+    a = layer_inputs(N, h, r, s, M, seed=5)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    d, pbar = rnd(g, N, h), torch.randn(M, generator=g, device="cuda") * 0.01
+    idx, gate, count, logits, m, Z, psum = more.route_train(a["X"], a["R1"], a["R2"], k)
+    offsets, slots = more.dispatch(idx, M)
+    out = more.experts(a["X"], a["W_up"], a["W_down"], gate, offsets, slots)
+    Xe, dU, dD, dg, dl = more.experts_backward(a["X"], a["W_up"], a["W_down"], gate, offsets, slots, d)
+    Xr, dR1, dR2, _ = more.route_backward(a["X"], a["R1"], a["R2"], k, top_idx=idx, top_vals_bar=dl, pbar=pbar, m=m, Z=Z)
+    assert ok() and torch.equal(count, offsets.diff())
+    ref.check(out, *ref.forward(a["X"], a["W_up"], a["W_down"], gate, offsets, slots), "out")
+    want, bound = ref.backward(a["X"], a["W_up"], a["W_down"], gate, offsets, slots, d)
+    for name, t in zip(want, (Xe, dU, dD, dg, dl)):
+        ref.check(t, want[name], bound[name], name)
+    # the router's part: autograd in 64 bits from the same gradient on the selected logits; 2e-3 of the terms' magnitudes
+    # is that kernel's own tolerance (its softmax and z are fp32)
+    X, R1, R2 = (a[n].double().requires_grad_() for n in ("X", "R1", "R2"))
+    l = X @ R1 @ R2
+    (l.gather(1, idx.long()) * dl.double()).sum().add((torch.softmax(l, 1).sum(0) * pbar.double()).sum()).backward()
+    y = torch.zeros_like(l).scatter_(1, idx.long(), dl.double().abs()) + torch.softmax(l, 1).detach() * 2 * pbar.abs().max()
+    z = y @ R2.detach().abs().T
+    mags = (z @ R1.detach().abs().T, X.detach().abs().T @ z, (X.detach().abs() @ R1.detach().abs()).T @ y)
+    for got, leaf, mag, name in zip((Xr, dR1, dR2), (X, R1, R2), mags, ("X", "R1", "R2")):
+        assert ((got.double() - leaf.grad).abs() <= 2e-3 * mag).all(), name
+
+
+def test_layer_of_more_tokens_is_the_three_calls():
+    import mixture_experts_rank_b200 as more
+    a = layer_inputs(130, 256, 32, 64, 32)
+    idx, gate, _, _ = more.route(a["X"], a["R1"], a["R2"], 4)
+    offsets, slots = more.dispatch(idx, 32)
+    assert torch.equal(more.moe_layer(**a, k=4), more.experts(a["X"], a["W_up"], a["W_down"], gate, offsets, slots))
