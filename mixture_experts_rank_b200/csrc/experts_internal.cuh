@@ -119,13 +119,15 @@ cudaError_t launch_quantize_bf16(const __nv_bfloat16* v, int64_t rows, int width
 cudaError_t launch_quantize_rows(const ExpertsArgs& a, const Rows& r, const float* v, int width, int8_t* q,
                                  float* scale, int tile_rows);
 
-// The whole layer of a few tokens (moe_layer.cu).  Xq and the scales: 8-bit weights.
+// The whole layer of a few tokens, or its experts alone (moe_layer.cu).  Xq and the scales: 8-bit weights.
 struct FewArgs {
   const void *X, *R1, *R2;
   int8_t* Xq;      // [N][h]
   float* x_scale;  // [N]
   const void *W_up, *W_down;
   const float *up_scale, *down_scale;
+  const int32_t *offsets, *slots;  // selections made before (with given_gate); null: routed by the call
+  const float* given_gate;
   float *z, *logits;  // [N][r], [N][M]
   int32_t* idx;       // [N k]
   float* gate;        // [N k]
@@ -141,6 +143,8 @@ struct FewArgs {
   cudaStream_t stream;
 };
 bool layer_few_fits(int64_t N, int h, int k);
+// The same kernel for selections that were dispatched before.
+bool experts_few_fits(int64_t N, int h, int M, int k);
 cudaError_t launch_layer_few(const FewArgs& f);
 
 size_t experts_scratch(int64_t N, int h, int s, int M, int k, int kind);  // kind: 0 bf16, 1 int8, 2 backward

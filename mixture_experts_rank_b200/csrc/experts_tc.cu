@@ -1123,6 +1123,7 @@ struct Buffers {
   void *Xr, *Dr;  // X's (or its 8 bits') and y_bar's rows in the padded layout, for CTA pairs
   float *x_scale, *row_scale, *h_scale, *part;
   __nv_bfloat16 *pre, *mid;
+  FewArgs few;  // the buffers of the few-token kernel
   size_t bytes;
 };
 
@@ -1142,6 +1143,21 @@ Buffers carve(void* scratch, int64_t N, int h, int s, int M, int k, int kind) {
   Carver c(scratch);
   const int64_t S = N * k, R = max_rows(S, M);
   const bool pair = takes_pairs(S, s, M);
+  if (kind != kBackward && experts_few_fits(N, h, M, k)) {
+    FewArgs& f = b.few;
+    f.barrier = c.take<unsigned int>(1);
+    if (kind == kForward) {
+      f.mid_pair = c.take<__nv_bfloat16>(2 * S * s);
+    } else {
+      f.mid = c.take<float>(S * s);
+      f.mid_q = c.take<int8_t>(S * s);
+      f.mid_scale = c.take<float>(S);
+      f.Xq = c.take<int8_t>(N * h);
+      f.x_scale = c.take<float>(N);
+    }
+    b.bytes = c.used;
+    return b;
+  }
   b.rows = carve_rows(c, S, M);
   if (kind == kForward) {
     if (pair) b.Xr = c.take<__nv_bfloat16>(R * h);
@@ -1174,8 +1190,31 @@ size_t experts_scratch(int64_t N, int h, int s, int M, int k, int kind) {
   return carve(nullptr, N, h, s, M, k, kind).bytes;
 }
 
+namespace {
+cudaError_t launch_few(const ExpertsArgs& a, FewArgs f) {
+  f.X = a.X;
+  f.W_up = a.W_up;
+  f.W_down = a.W_down;
+  f.up_scale = a.up_scale;
+  f.down_scale = a.down_scale;
+  f.offsets = a.offsets;
+  f.slots = a.slots;
+  f.given_gate = a.gate;
+  f.out = a.out;
+  f.N = a.N;
+  f.h = a.h;
+  f.s = a.s;
+  f.M = a.M;
+  f.k = a.k;
+  f.status = a.status;
+  f.stream = a.stream;
+  return launch_layer_few(f);
+}
+}  // namespace
+
 cudaError_t launch_experts(const ExpertsArgs& a) {
   const Buffers b = carve(a.scratch, a.N, a.h, a.s, a.M, a.k, kForward);
+  if (experts_few_fits(a.N, a.h, a.M, a.k)) return launch_few(a, b.few);
   const bool pair = takes_pairs(a.S(), a.s, a.M);
   MORE_TRY(launch_rows(a, b.rows, pair ? 2 * kTileRows : kTileRows));
   if (pair) MORE_TRY(launch_pick(a, b.rows, a.X, 2 * a.h, b.Xr));
@@ -1186,6 +1225,7 @@ cudaError_t launch_experts(const ExpertsArgs& a) {
 
 cudaError_t launch_experts_int8(const ExpertsArgs& a) {
   const Buffers b = carve(a.scratch, a.N, a.h, a.s, a.M, a.k, kInt8);
+  if (experts_few_fits(a.N, a.h, a.M, a.k)) return launch_few(a, b.few);
   const bool pair = takes_pairs(a.S(), a.s, a.M);
   MORE_TRY(launch_quantize_bf16(static_cast<const __nv_bfloat16*>(a.X), a.N, a.h, static_cast<int8_t*>(b.Xq),
                                 b.x_scale, a.stream));

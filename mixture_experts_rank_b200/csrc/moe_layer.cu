@@ -39,6 +39,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 8;  // selections of one expert that share a reading of its weights: the columns of an MMA
 constexpr int kRows = 16;  // rows of an MMA
 constexpr int64_t kFewTokens = 64;
+constexpr int kFewExperts = 16384;  // every CTA reads all the offsets of a dispatch
 constexpr int kSolo = 2;         // tokens that every CTA routes for itself
 constexpr int kSlots = 4;                   // batches of a warp's ring
 constexpr uint32_t kRing = 128 * 1024;      // all warps' rings
@@ -51,6 +52,8 @@ struct LayerArgs {
   float* x_scale;
   const void *W_up, *W_down;
   const float *up_scale, *down_scale;
+  const int32_t *offsets, *slots;  // selections that were made and dispatched before the call; null: routed here
+  const float* given_gate;
   float* z;       // [N][r]
   float* logits;  // [N][M]
   int32_t* idx;   // [S]
@@ -392,7 +395,39 @@ __device__ __forceinline__ int place_of(int32_t* keys, int key) {
   return 0;  // not reached: at most 1024 keys
 }
 
-__device__ int group_selections(const LayerArgs& a, const Shared& sh, bool solo, int* warp_sums) {
+// The selections of a dispatch, into shared memory.  As in the row layout of the grouped products, offsets that fall or lie
+// outside [0, S] leave nothing, and a slot outside [0, S) is skipped.
+__device__ void read_dispatch(const LayerArgs& a, const Shared& sh) {
+  for (int i = threadIdx.x; i < a.S; i += kThreads) {
+    sh.expert[i] = -1;
+    sh.gate[i] = a.given_gate[i];
+  }
+  int broken = 0;
+#pragma unroll 4
+  for (int e = threadIdx.x; e < a.M; e += kThreads) {
+    const int b = __ldg(a.offsets + e), c = __ldg(a.offsets + e + 1);
+    broken |= b < 0 || c < b || c > a.S;
+  }
+  const bool none = __syncthreads_or(broken);
+  bool bad = none;
+  if (!none) {
+    for (int e = threadIdx.x; e < a.M; e += kThreads) {
+      const int c = __ldg(a.offsets + e + 1);
+      for (int i = __ldg(a.offsets + e); i < c; ++i) {
+        const int slot = __ldg(a.slots + i);
+        if (slot >= 0 && slot < a.S)
+          sh.expert[slot] = e;
+        else
+          bad = true;
+      }
+    }
+  }
+  if (bad && blockIdx.x == 0) atomicOr(a.status, MORE_DEVERR_BAD_INPUT);
+  __syncthreads();
+}
+
+// `here`: the selections are in shared memory.
+__device__ int group_selections(const LayerArgs& a, const Shared& sh, bool here, int* warp_sums) {
   int32_t* t_expert = reinterpret_cast<int32_t*>(sh.work);
   int32_t* t_count = t_expert + kTable;
   int32_t* t_first = t_count + kTable;
@@ -400,10 +435,10 @@ __device__ int group_selections(const LayerArgs& a, const Shared& sh, bool solo,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (a.S <= 32) {  // one warp's lanes find one another
     if (warp == 0) {
-      int e = lane < a.S ? (solo ? sh.expert[lane] : a.idx[lane]) : -1;
-      if (!solo && lane < a.S) sh.gate[lane] = a.gate[lane];
+      int e = lane < a.S ? (here ? sh.expert[lane] : a.idx[lane]) : -1;
+      if (!here && lane < a.S) sh.gate[lane] = a.gate[lane];
       const bool ok = e >= 0 && e < a.M;
-      if (!ok && lane < a.S && blockIdx.x == 0) atomicOr(a.status, MORE_DEVERR_BAD_INPUT);
+      if (!ok && lane < a.S && !a.offsets && blockIdx.x == 0) atomicOr(a.status, MORE_DEVERR_BAD_INPUT);
       if (!ok) e = -1;
       if (lane < a.S) sh.expert[lane] = e;
       const unsigned same = __match_any_sync(0xffffffffu, e);
@@ -434,10 +469,10 @@ __device__ int group_selections(const LayerArgs& a, const Shared& sh, bool solo,
     t_first[i] = 0x7fffffff;
   }
   for (int i = threadIdx.x; i < a.S; i += kThreads) {
-    const int e = solo ? sh.expert[i] : a.idx[i];
-    if (!solo) sh.gate[i] = a.gate[i];
+    const int e = here ? sh.expert[i] : a.idx[i];
+    if (!here) sh.gate[i] = a.gate[i];
     const bool ok = e >= 0 && e < a.M;
-    if (!ok && blockIdx.x == 0) atomicOr(a.status, MORE_DEVERR_BAD_INPUT);
+    if (!ok && !a.offsets && blockIdx.x == 0) atomicOr(a.status, MORE_DEVERR_BAD_INPUT);
     sh.expert[i] = ok ? e : -1;
   }
   __syncthreads();
@@ -759,9 +794,10 @@ struct Down {
   const Shared& sh;
   int o0, rows, tiles, units, batches, pitch, lane, warp, pc, r0;
   R ring;
-  int fu, fb;
+  int fu, fb, left = 0;
   const uint8_t* from;
 
+  __device__ __forceinline__ int group_of(int u) const { return tiles == 1 ? u : u / tiles; }
   __device__ Down(const LayerArgs& a_, const Shared& sh_, int groups, int rows_each) : a(a_), sh(sh_) {
     warp = threadIdx.x >> 5;
     lane = threadIdx.x & 31;
@@ -780,13 +816,14 @@ struct Down {
   }
   __device__ __forceinline__ void locate() {
     if (fu >= units) return;
-    const int g = fu / tiles, r = (fu - g * tiles) * kRows + r0;
+    const int g = group_of(fu), r = (fu - g * tiles) * kRows + r0;
+    left = rows - r;
     from = static_cast<const uint8_t*>(a.W_down) + ((size_t)sh.group_e[g] * a.h + o0 + r) * pitch + pc * 16;
   }
   __device__ __forceinline__ void fetch() {
     const uint32_t at = ring.fill() + R::place(r0, pc);
     if (fu < units) {
-      const int off = fb * (int)R::kBatch, left = rows - fu % tiles * kRows - r0;
+      const int off = fb * (int)R::kBatch;
       if (off + pc * 16 < pitch) {
 #pragma unroll
         for (int i = 0; i < 16 / R::kAtOnce; ++i)
@@ -809,7 +846,7 @@ struct Down {
     for (int i = threadIdx.x; i < a.S * rows; i += kThreads) sh.y[i] = 0.f;  // selections of no expert stay zero
   }
   __device__ __forceinline__ size_t middle_of(int u) const {
-    const int g = u / tiles;
+    const int g = group_of(u);
     return (size_t)sh.member[g * kGroup + min(lane >> 2, sh.group_n[g] - 1)] * pitch + (lane & 3) * 16;
   }
   __device__ __forceinline__ void load(size_t at, int b, uint4 (&hi)[BS], uint4 (&lo)[BS]) const {
@@ -837,7 +874,7 @@ struct Down {
     }
 #pragma unroll 1
     for (int u = warp; u < units; u += R::kStreams) {
-      const int g = u / tiles, r = (u - g * tiles) * kRows + row, n = sh.group_n[g];
+      const int g = group_of(u), r = (u - g * tiles) * kRows + row, n = sh.group_n[g];
       Sums<I8> c = {};
 #pragma unroll 1
       for (int b = 0; b < batches; ++b) {
@@ -854,13 +891,14 @@ struct Down {
         }
         const uint32_t at = ring.drain() + row * R::kBatch;
         fetch();
+        const bool tail = (b + 1) * (int)R::kBatch > pitch;
 #pragma unroll
         for (int j = 0; j < BS; ++j) {
           const uint32_t q = (uint32_t)(piece + 64 * j) ^ ((row & 1) << 6);
-          const bool in = b * (int)R::kBatch + 64 * j + piece < pitch;
+          // bytes behind a row's end multiply zeros and have to be numbers; rows behind the last only spoil themselves
+          const bool in = !tail || b * (int)R::kBatch + 64 * j + piece < pitch;
           uint4 w0 = sm100::ld_shared_v4(at + q), w1 = sm100::ld_shared_v4(at + 8 * R::kBatch + q);
-          if (!in || r >= rows) w0 = make_uint4(0, 0, 0, 0);
-          if (!in || r + 8 >= rows) w1 = make_uint4(0, 0, 0, 0);
+          if (!in) w0 = w1 = make_uint4(0, 0, 0, 0);
           step_products<I8>(c, w0, w1, hi[j]);
           if constexpr (!I8) step_products<I8>(c, w0, w1, lo[j]);
         }
@@ -914,18 +952,21 @@ __global__ void __launch_bounds__(kThreads, 1) layer_kernel(const __grid_constan
   const Shared sh = shared_at(smem, a.S);
   unsigned turn = 0;
   if constexpr (I8) round_tokens(a, u.tops);
-  project_tokens(a, u.part);
-  if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
-  expert_logits(a, reinterpret_cast<float*>(sh.work));
-  if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
-  const bool solo = a.N <= kSolo;
-  if (solo) {
-    for (int n = 0; n < a.N; ++n) select_experts(a, n, u.select, sh.expert, sh.gate);
+  bool here = true;
+  if (a.offsets) {
+    read_dispatch(a, sh);
+    if (I8 && !grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
   } else {
-    for (int n = blockIdx.x; n < a.N; n += gridDim.x) select_experts(a, n, u.select, a.idx, a.gate);
+    project_tokens(a, u.part);
     if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
+    expert_logits(a, reinterpret_cast<float*>(sh.work));
+    if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
+    here = a.N <= kSolo;
+    for (int n = here ? 0 : blockIdx.x; n < a.N; n += here ? 1 : gridDim.x)
+      select_experts(a, n, u.select, here ? sh.expert : a.idx, here ? sh.gate : a.gate);
+    if (!here && !grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
   }
-  const int groups = group_selections(a, sh, solo, warp_sums);
+  const int groups = group_selections(a, sh, here, warp_sums);
   up_phase<I8>(a, sh, groups, u.red);
   if constexpr (I8) {
     if (!grid_barrier(a.barrier, ++turn, a.status, &failed)) return;
@@ -975,6 +1016,8 @@ cudaError_t launch_layer(const LayerArgs& a, cudaStream_t stream) {
 
 // The few-token kernel takes the shape: its shared memory holds the selections' output channels (a CTA's share of h,
 // at least 132 CTAs assumed), and a batch of up to kFewTokens tokens.
+bool experts_few_fits(int64_t N, int h, int M, int k) { return N > 0 && M <= kFewExperts && layer_few_fits(N, h, k); }
+
 bool layer_few_fits(int64_t N, int h, int k) {
   return N <= kFewTokens && layer_smem((int)(N * k), (h + 131) / 132) <= kSmemMost;
 }
@@ -990,6 +1033,9 @@ cudaError_t launch_layer_few(const FewArgs& f) {
   a.W_down = f.W_down;
   a.up_scale = f.up_scale;
   a.down_scale = f.down_scale;
+  a.offsets = f.offsets;
+  a.slots = f.slots;
+  a.given_gate = f.given_gate;
   a.z = f.z;
   a.logits = f.logits;
   a.idx = f.idx;
