@@ -47,6 +47,7 @@ __device__ void scan_pairs(int& rows, int& tiles, int* warp_rows, int* warp_tile
 __global__ void __launch_bounds__(kScanThreads)
     rows_scan_kernel(const int32_t* __restrict__ offsets, int64_t S, int M, int tile_rows, Rows out,
                      unsigned int* status) {
+  after_previous();
   __shared__ int warp_rows[kScanThreads / 32], warp_tiles[kScanThreads / 32];
   __shared__ int bad;
   const int run = (M + kScanThreads - 1) / kScanThreads;
@@ -96,6 +97,7 @@ __global__ void __launch_bounds__(2 * kTileRows)
     rows_fill_kernel(const int32_t* __restrict__ offsets, const int32_t* __restrict__ slots,
                      const float* __restrict__ gate, int64_t S, int k, const float* __restrict__ token_scale,
                      float* __restrict__ row_scale, Rows out, unsigned int* status) {
+  after_previous();
   if ((int)blockIdx.x >= *out.n_tiles) return;
   const int4 t = out.tiles[blockIdx.x];
   const int r = threadIdx.x;
@@ -138,6 +140,7 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 __global__ void __launch_bounds__(256)
     combine_kernel(const __nv_bfloat16* __restrict__ y, const int32_t* __restrict__ slot_row, int64_t N, int h, int k,
                    int log_across, __nv_bfloat16* __restrict__ out) {
+  after_previous();
   const int groups = h >> 3, across = 1 << log_across;
   const int64_t n = (int64_t)blockIdx.x * (256 >> log_across) + (threadIdx.x >> log_across);
   if (n >= N) return;
@@ -162,6 +165,7 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(256)
     pick_kernel(const uint4* __restrict__ src, const int32_t* __restrict__ row_token, const int32_t* __restrict__ rows,
                 int pieces, uint4* __restrict__ dst) {
+  after_previous();
   const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= *rows) return;
@@ -183,6 +187,7 @@ __global__ void __launch_bounds__(256)
     gate_grads_kernel(const float* __restrict__ part, int parts, int64_t R, const int32_t* __restrict__ slot_row,
                       const float* __restrict__ gate, int64_t N, int k, float* __restrict__ gate_bar,
                       float* __restrict__ logits_bar) {
+  after_previous();
   const int64_t n = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
   const int j = threadIdx.x & 15;
   const bool in = n < N && j < k;
@@ -234,6 +239,7 @@ __device__ __forceinline__ uint2 round8x8(uint4 w, float div, float inv) {
 __global__ void __launch_bounds__(128, 8)
     quantize_bf16_kernel(const __nv_bfloat16* __restrict__ v, int64_t rows, int width, int8_t* __restrict__ q,
                          float* __restrict__ scale) {
+  after_previous();
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
@@ -268,6 +274,7 @@ constexpr int kRowsPerBlock = 32;
 __global__ void __launch_bounds__(256)
     quantize_rows_kernel(const float* __restrict__ v, int width, Rows r, int8_t* __restrict__ q,
                          float* __restrict__ scale) {
+  after_previous();
   const int lane = threadIdx.x & 31;
   if ((int)blockIdx.x >= *r.n_tiles) return;
   const int4 t = r.tiles[blockIdx.x];
@@ -318,16 +325,15 @@ cudaError_t launch_rows(const ExpertsArgs& a, const Rows& r, int tile_rows, cons
   const int64_t S = a.S();
   cudaError_t e = cudaMemsetAsync(r.slot_row, 0xff, sizeof(int32_t) * (size_t)S, a.stream);
   if (e != cudaSuccess) return e;
-  rows_scan_kernel<<<1, kScanThreads, 0, a.stream>>>(a.offsets, S, a.M, tile_rows, r, a.status);
-  rows_fill_kernel<<<(unsigned)max_tiles(S, a.M, tile_rows), tile_rows, 0, a.stream>>>(
-      a.offsets, a.slots, a.gate, S, a.k, token_scale, row_scale, r, a.status);
-  return cudaGetLastError();
+  e = launch_next(rows_scan_kernel, dim3(1), dim3(kScanThreads), 0, a.stream, 1, a.offsets, S, a.M, tile_rows, r, a.status);
+  if (e != cudaSuccess) return e;
+  return launch_next(rows_fill_kernel, dim3((unsigned)max_tiles(S, a.M, tile_rows)), dim3(tile_rows), 0, a.stream, 1,
+                     a.offsets, a.slots, a.gate, S, a.k, token_scale, row_scale, r, a.status);
 }
 
 cudaError_t launch_pick(const ExpertsArgs& a, const Rows& r, const void* src, int pitch, void* dst) {
-  pick_kernel<<<(unsigned)(max_rows(a.S(), a.M) / 8), 256, 0, a.stream>>>(
-      static_cast<const uint4*>(src), r.row_token, r.row_start + a.M, pitch / 16, static_cast<uint4*>(dst));
-  return cudaGetLastError();
+  return launch_next(pick_kernel, dim3((unsigned)(max_rows(a.S(), a.M) / 8)), dim3(256), 0, a.stream, 1,
+                     static_cast<const uint4*>(src), r.row_token, r.row_start + a.M, pitch / 16, static_cast<uint4*>(dst));
 }
 
 cudaError_t launch_combine(const ExpertsArgs& a, const Rows& r, const __nv_bfloat16* y, void* out) {
@@ -343,29 +349,26 @@ cudaError_t launch_combine(const ExpertsArgs& a, const Rows& r, const __nv_bfloa
     }
   }
   const int tokens = 256 >> log_across;
-  combine_kernel<<<(unsigned)((a.N + tokens - 1) / tokens), 256, 0, a.stream>>>(
-      y, r.slot_row, a.N, a.h, a.k, log_across, static_cast<__nv_bfloat16*>(out));
-  return cudaGetLastError();
+  return launch_next(combine_kernel, dim3((unsigned)((a.N + tokens - 1) / tokens)), dim3(256), 0, a.stream, 1, y,
+                     r.slot_row, a.N, a.h, a.k, log_across, static_cast<__nv_bfloat16*>(out));
 }
 
 cudaError_t launch_gate_grads(const ExpertsArgs& a, const Rows& r, const float* part, int parts, int64_t R) {
-  gate_grads_kernel<<<(unsigned)((a.N + 15) / 16), 256, 0, a.stream>>>(part, parts, R, r.slot_row, a.gate, a.N, a.k,
-                                                                          a.gate_bar, a.logits_bar);
-  return cudaGetLastError();
+  return launch_next(gate_grads_kernel, dim3((unsigned)((a.N + 15) / 16)), dim3(256), 0, a.stream, 1, part, parts, R,
+                     r.slot_row, a.gate, a.N, a.k, a.gate_bar, a.logits_bar);
 }
 
 cudaError_t launch_quantize_bf16(const __nv_bfloat16* v, int64_t rows, int width, int8_t* q, float* scale,
                                  cudaStream_t stream) {
   if (rows == 0) return cudaSuccess;
-  quantize_bf16_kernel<<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(v, rows, width, q, scale);
-  return cudaGetLastError();
+  return launch_next(quantize_bf16_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, 1, v, rows, width, q,
+                     scale);
 }
 
 cudaError_t launch_quantize_rows(const ExpertsArgs& a, const Rows& r, const float* v, int width, int8_t* q,
                                  float* scale, int tile_rows) {
   const dim3 grid((unsigned)max_tiles(a.S(), a.M, tile_rows), tile_rows / kRowsPerBlock);
-  quantize_rows_kernel<<<grid, 256, 0, a.stream>>>(v, width, r, q, scale);
-  return cudaGetLastError();
+  return launch_next(quantize_rows_kernel, grid, dim3(256), 0, a.stream, 1, v, width, r, q, scale);
 }
 
 }  // namespace more

@@ -962,6 +962,7 @@ __global__ void __launch_bounds__(Shape<MODE, HALF, PAIR>::kThreads, 1)
   if constexpr (PAIR) cluster_sync_all();  // the other CTA's barriers are used from here on
   tc_fence_after();
   const uint32_t tmem = *b.tmem_slot;
+  after_previous();
   if (warp == 0) {
     box_loads<MODE, HALF, PAIR>(p, b, smem, &m0, &m1, &m2, &m3, rank);
     __syncwarp();
@@ -1037,18 +1038,8 @@ cudaError_t launch(const ExpertsArgs& a, Params p, int64_t items, const CUtensor
   p.status = a.status;
   constexpr int ctas = PAIR ? 2 : 1;
   const int64_t most = sms / ctas;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((items < most ? items : most) * ctas));
-  cfg.blockDim = dim3(S::kThreads);
-  cfg.dynamicSmemBytes = S::kSmem;
-  cfg.stream = a.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, grouped_kernel<MODE, HALF, PAIR>, m0, m1, m2, m3, p);
+  return launch_next(grouped_kernel<MODE, HALF, PAIR>, dim3((unsigned)((items < most ? items : most) * ctas)),
+                     dim3(S::kThreads), S::kSmem, a.stream, ctas, m0, m1, m2, m3, p);
 }
 
 int tiles_of(int n, int bn) { return (n + bn - 1) / bn; }
