@@ -327,9 +327,9 @@ more_status more_route_backward(const void* X, const void* R1, const void* R2, i
  *   offsets  int32 [M + 1], slots int32 [N k]   as more_dispatch writes them; a slot is listed at most once
  *   out      bf16 [N][h]        overwritten; a token none of whose slots is listed gets zeros
  * Both products are accumulated in fp32; silu(A x) * (B x) and each slot's row of the second product, already
- * times its gate, are rounded to bf16, and a token's k rows are summed in fp32 in the order of j.  Up to 64 tokens (and
- * M <= 16384) run in the one kernel of more_moe_layer, which carries the former as a bf16 pair (about 16 bits) and the
- * latter in fp32.  The result does not depend on the launch.
+ * times its gate, are rounded to bf16, and a token's k rows are summed in fp32 in the order of j.  Up to 16
+ * tokens, or 64 with N k <= M (and M <= 16384), run in the one kernel of more_moe_layer, which carries the former as a
+ * bf16 pair (about 16 bits) and the latter in fp32.  The result does not depend on the launch.
  * Offsets that fall or lie outside [0, N k] give zeros, and a slot outside [0, N k) is skipped; both set
  * MORE_DEVERR_BAD_INPUT.
  * scratch: device, 16-byte aligned, at least more_experts_scratch_bytes(N, h, s, M, k) bytes (0: not supported); calls

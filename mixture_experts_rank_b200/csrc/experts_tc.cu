@@ -1125,15 +1125,25 @@ enum Kind { kForward = 0, kInt8 = 1, kBackward = 2 };
 int back_half(int h, int s) { return s <= 64 || h > 2 * kRun ? 64 : 128; }
 int gate_parts(int h, int s) { return 2 * tiles_of(s, back_half(h, s)); }
 
-// CTA pairs with 256-row tiles, the rows picked by token copied together first.  For wide experts with enough rows to
-// fill such tiles; narrow ones read each picked row once anyway, and are bound by memory.
-bool takes_pairs(int64_t S, int s, int M) { return s > 128 && S >= 192 * (int64_t)M; }
+// CTA pairs with 256-row tiles, the rows picked by token copied together first (the copies by token of a pair would
+// need both CTAs' loaders).  A pair reads the weights once for 256 rows, but the picked rows are written and read once
+// more, and tiles of 256 waste more of the last one.  us a call with and without pairs, for T rows an expert:
+//   forward   h = 2048: s = 256, T = 1024: 188, 153    s = 512, T = 1024: 136, 128    s = 1024, T = 2048: 428, 403
+//             s = 2048, T = 1024: 193, 202             h = 1096, s = 712, T = 469: 244, 265
+//             h = 4096, s = 4096, T = 1024: 336, 372
+//   8 bits    h = 2048: s = 512, T = 1024: 138, 126    s = 2048, T = 1500: 961, 1048    h = 2880 = s, T = 1024: 293, 339
+//   backward  h = 1024: s = 144, T = 512: 437, 405     s = 512, T = 1024: 381, 409     s = 1024, T = 192: 216, 231
+//             s = 1024, T = 128: 206, 200              h = 2048, s = 1024, T = 2048: 1245, 1469
+//             h = 4096 (its first kernel takes no pairs): s = 512: 435, 428    s = 1024: 762, 785
+bool takes_pairs(int64_t S, int h, int s, int M, int kind) {
+  return S >= 192 * (int64_t)M && s >= (kind == kBackward && h <= 2 * kRun ? 512 : 704);
+}
 
 Buffers carve(void* scratch, int64_t N, int h, int s, int M, int k, int kind) {
   Buffers b = {};
   Carver c(scratch);
   const int64_t S = N * k, R = max_rows(S, M);
-  const bool pair = takes_pairs(S, s, M);
+  const bool pair = takes_pairs(S, h, s, M, kind);
   if (kind != kBackward && experts_few_fits(N, h, M, k)) {
     FewArgs& f = b.few;
     f.barrier = c.take<unsigned int>(1);
@@ -1206,7 +1216,7 @@ cudaError_t launch_few(const ExpertsArgs& a, FewArgs f) {
 cudaError_t launch_experts(const ExpertsArgs& a) {
   const Buffers b = carve(a.scratch, a.N, a.h, a.s, a.M, a.k, kForward);
   if (experts_few_fits(a.N, a.h, a.M, a.k)) return launch_few(a, b.few);
-  const bool pair = takes_pairs(a.S(), a.s, a.M);
+  const bool pair = takes_pairs(a.S(), a.h, a.s, a.M, kForward);
   MORE_TRY(launch_rows(a, b.rows, pair ? 2 * kTileRows : kTileRows));
   if (pair) MORE_TRY(launch_pick(a, b.rows, a.X, 2 * a.h, b.Xr));
   MORE_TRY(run_up<kUp>(a, b.rows, pair ? b.Xr : a.X, nullptr, b.H, nullptr, pair));
@@ -1217,7 +1227,7 @@ cudaError_t launch_experts(const ExpertsArgs& a) {
 cudaError_t launch_experts_int8(const ExpertsArgs& a) {
   const Buffers b = carve(a.scratch, a.N, a.h, a.s, a.M, a.k, kInt8);
   if (experts_few_fits(a.N, a.h, a.M, a.k)) return launch_few(a, b.few);
-  const bool pair = takes_pairs(a.S(), a.s, a.M);
+  const bool pair = takes_pairs(a.S(), a.h, a.s, a.M, kInt8);
   MORE_TRY(launch_quantize_bf16(static_cast<const __nv_bfloat16*>(a.X), a.N, a.h, static_cast<int8_t*>(b.Xq),
                                 b.x_scale, a.stream));
   MORE_TRY(launch_rows(a, b.rows, pair ? 2 * kTileRows : kTileRows, b.x_scale, b.row_scale));
@@ -1236,7 +1246,7 @@ cudaError_t launch_experts_int8(const ExpertsArgs& a) {
 cudaError_t launch_experts_backward(const ExpertsArgs& a) {
   const Buffers b = carve(a.scratch, a.N, a.h, a.s, a.M, a.k, kBackward);
   const int64_t S = a.S(), R = max_rows(S, a.M);
-  const bool pair = takes_pairs(S, a.s, a.M);
+  const bool pair = takes_pairs(S, a.h, a.s, a.M, kBackward);
   const int rows = pair ? 2 * kTileRows : kTileRows;
   const int64_t tiles = max_tiles(S, a.M, rows);
   const int half = back_half(a.h, a.s);

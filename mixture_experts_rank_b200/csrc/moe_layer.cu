@@ -39,6 +39,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 8;  // selections of one expert that share a reading of its weights: the columns of an MMA
 constexpr int kRows = 16;  // rows of an MMA
 constexpr int64_t kFewTokens = 64;
+constexpr int64_t kFewRows = 16;  // tokens up to which the experts alone run here whatever they share
 constexpr int kFewExperts = 16384;  // every CTA reads all the offsets of a dispatch
 constexpr int kSolo = 2;         // tokens that every CTA routes for itself
 constexpr int kSlots = 4;                   // batches of a warp's ring
@@ -1015,8 +1016,16 @@ cudaError_t launch_layer(const LayerArgs& a, cudaStream_t stream) {
 }  // namespace
 
 // The few-token kernel takes the shape: its shared memory holds the selections' output channels (a CTA's share of h,
-// at least 132 CTAs assumed), and a batch of up to kFewTokens tokens.
-bool experts_few_fits(int64_t N, int h, int M, int k) { return N > 0 && M <= kFewExperts && layer_few_fits(N, h, k); }
+// at least 132 CTAs assumed), and a batch of up to kFewTokens tokens.  The layer gains by it up to there: it saves the
+// router's launches too (N = 64: h = 2048, s = 64, M = 4096, k = 8: 98 us against 139; 1024, 256, 128, 4: 67 against
+// 81; only weights of 0.8 GB, 2048, 1024, 64, 4, take 186 against 177).
+// The experts alone gain while the selections seldom share an expert, whose weights this kernel then reads at 4 TB/s in
+// one launch, and the grouped products at 5.8 after five launches.  us, few against grouped:
+//   2048, 64, 4096, 8:   N = 8: 25, 39    N = 64: 87, 94        2048, 1024, 64, 4:  N = 16: 107, 108    N = 32: 137, 122
+//   512, 64, 1024, 4:    N = 8: 18, 26    N = 64: 31, 30        1024, 256, 128, 4:  N = 32: 49, 48      N = 64: 59, 51
+bool experts_few_fits(int64_t N, int h, int M, int k) {
+  return N > 0 && M <= kFewExperts && (N <= kFewRows || N * k <= M) && layer_few_fits(N, h, k);
+}
 
 bool layer_few_fits(int64_t N, int h, int k) {
   return N <= kFewTokens && layer_smem((int)(N * k), (h + 131) / 132) <= kSmemMost;

@@ -12,13 +12,17 @@ SIZES = [  # N, h, s, M, k
     (1, 8, 8, 8, 1), (1, 64, 16, 8, 8), (2, 2048, 64, 64, 8), (37, 72, 24, 16, 3), (300, 136, 200, 8, 2),
     (130, 520, 64, 40, 5), (1000, 256, 72, 24, 4), (129, 64, 264, 1, 1), (513, 320, 136, 3, 2), (700, 1096, 392, 8, 3),
     (64, 128, 64, 1000, 16),
+    (40, 128, 64, 1000, 16), (17, 128, 72, 16, 4), (16, 128, 72, 4, 4),  # few selections an expert, or few tokens
     (260, 1024, 160, 1, 1), (1500, 264, 1032, 4, 2), (3000, 200, 136, 16, 3),  # wide experts with many rows: CTA pairs
+    (193, 1096, 712, 1, 1), (900, 72, 704, 4, 2), (600, 520, 520, 3, 2), (420, 2120, 712, 1, 1),
     (70, 4104, 56, 4, 2), (500, 2112, 136, 2, 1),  # h long enough for sums in runs
 ]
 SIZES_8 = [  # the same with h and s in whole 16s
     (1, 16, 16, 8, 1), (1, 64, 16, 8, 8), (2, 2048, 64, 64, 8), (37, 80, 48, 16, 3), (300, 144, 208, 8, 2),
     (130, 528, 64, 40, 5), (129, 64, 272, 1, 1), (513, 320, 144, 3, 2), (700, 1104, 400, 8, 3), (64, 128, 64, 1000, 16),
+    (40, 128, 64, 1000, 16), (17, 128, 80, 16, 4), (16, 128, 80, 4, 4),
     (260, 1024, 160, 1, 1), (1500, 272, 1040, 4, 2), (3000, 208, 144, 16, 3),
+    (193, 1104, 720, 1, 1), (900, 80, 704, 4, 2), (420, 2128, 720, 1, 1),
 ]
 
 
@@ -269,7 +273,7 @@ def every_call(seed=0):
     """(name, call with given outputs) of each entry point, on inputs of its own."""
     import mixture_experts_rank_b200 as more
     args, d = make(300, 136, 72, 8, 2, seed)
-    wide, dw = make(600, 320, 136, 3, 2, seed)
+    wide, dw = make(600, 320, 712, 3, 2, seed)
     eight = int8_of(make(300, 144, 80, 8, 2, seed)[0])
     few = layer_inputs(7, 144, 16, 48, 24, seed)
     many = layer_inputs(90, 144, 16, 48, 24, seed)
