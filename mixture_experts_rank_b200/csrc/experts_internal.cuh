@@ -3,7 +3,8 @@
 //
 // The slots sorted by expert (more_dispatch) are laid out as rows, each expert's rows starting at a
 // multiple of 16 (kRowPad: the K step of a 16-bit MMA, so that a product over an expert's rows can
-// end on a whole step).  A tile is up to 128 rows of one expert, 256 for CTA pairs.  Padding rows repeat the expert's last token and carry slot -1.
+// end on a whole step).  A tile is up to 128 rows of one expert, 256 for CTA pairs.  Padding rows repeat
+// the expert's last token and carry slot -1.
 #pragma once
 #include "more_internal.cuh"
 
@@ -93,11 +94,12 @@ inline Rows carve_rows(Carver& c, int64_t S, int M) {
 // round-half-even(127 v / top) for |v| <= top, with `inv` = 127 / top.  127 v is exact for a bf16 v, so the division
 // would round no value across a half; the product with inv is off by less than 127 * 3 * 2^-24 < 2.3e-5, and only a
 // product that close to a half is divided.  Adding 1.5 * 2^23 rounds to a whole number in the mantissa's low bits: the
-// conversion instructions run at an eighth of the rate.
+// conversion instructions run at an eighth of the rate.  Where top is below 127 / FLT_MAX, inv is infinite and y no number:
+// those are divided too.
 __device__ __forceinline__ int8_t round8(float v, float top, float inv) {
   const float y = v * inv;
   float t = y + 12582912.f;
-  if (fabsf(fabsf(y - (t - 12582912.f)) - 0.5f) < 4e-5f) t = __fdiv_rn(127.f * v, top) + 12582912.f;
+  if (!(fabsf(fabsf(y - (t - 12582912.f)) - 0.5f) >= 4e-5f)) t = __fdiv_rn(127.f * v, top) + 12582912.f;
   return (int8_t)__float_as_int(t);
 }
 

@@ -425,6 +425,8 @@ __device__ void read_dispatch(const LayerArgs& a, const Shared& sh) {
   }
   if (bad && blockIdx.x == 0) atomicOr(a.status, MORE_DEVERR_BAD_INPUT);
   __syncthreads();
+  for (int i = threadIdx.x; i < a.S; i += kThreads)
+    if (sh.expert[i] < 0) sh.gate[i] = 0.f;  // its row is zero, and its gate may be no number
 }
 
 // `here`: the selections are in shared memory.
@@ -624,7 +626,8 @@ __device__ __forceinline__ void finish_up(const LayerArgs& a, const Shared& sh, 
     } else {
       const __nv_bfloat16 hi = __float2bfloat16_rn(m);
       a.mid_hi[at] = hi;
-      a.mid_lo[at] = __float2bfloat16_rn(m - __bfloat162float(hi));
+      const float rest = m - __bfloat162float(hi);
+      a.mid_lo[at] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.f);  // an infinite m is all in its first half
     }
   }
 }

@@ -98,6 +98,35 @@ def test_quantize_rows_is_exact(rows, width):
     assert ((scale.double() - sc[:, 0]).abs() <= 2.0**-24 * sc[:, 0]).all()
 
 
+@pytest.mark.parametrize("top", [2.0**-100, 2.0**-122, 2.0**-124, 2.0**-126, 2.0**-130, 2.0**-133])
+def test_quantize_rows_of_tiny_values(top):
+    """Rows whose 127 / max overflows, down to the smallest bf16: 2^-133 is one step of its subnormals."""
+    import mixture_experts_rank_b200 as more
+    steps = torch.arange(-8, 8, device="cuda", dtype=torch.float64)
+    V = (steps / 8 * top).to(torch.bfloat16)[None].repeat(3, 3)
+    V[1] = top
+    V[2, 1:] = 0
+    q, scale = more.quantize_rows(V)
+    assert ok()
+    want, sc, _ = ref.to_8_bits(V.double())
+    assert torch.equal(q.double(), want)
+    # a rounding to fp32: half a step relative to the value, or half the subnormals' step
+    assert ((scale.double() - sc[:, 0]).abs() <= 2.0**-24 * sc[:, 0] + 2.0**-150).all()
+
+
+@pytest.mark.parametrize("N", [9, 300])
+def test_tiny_tokens_among_ordinary_ones_in_8_bits(N):
+    import mixture_experts_rank_b200 as more
+    args = int8_of(make(N, 144, 80, 8, 2)[0])
+    want = more.experts_int8(**args)
+    X = args["X"].clone()
+    X[::3] = (X[::3].double() * 2.0**-126).bfloat16()
+    out = more.experts_int8(**dict(args, X=X))
+    assert ok()
+    assert torch.equal(out[1::3], want[1::3]) and torch.equal(out[2::3], want[2::3])
+    assert (out[::3].abs() < 2.0**-100).all()
+
+
 @pytest.mark.parametrize("how", ["spread", "first"])
 @pytest.mark.parametrize("size", SIZES_8, ids=str)
 def test_experts_int8(size, how):
@@ -267,6 +296,29 @@ def test_layer_with_equal_logits_takes_the_lowest_experts(M, k):
     out = more.moe_layer(**a, k=k)
     assert ok()
     ref.check(out, *layer_reference(a, k, True), "out")
+
+
+@pytest.mark.parametrize("N", [9, 300])
+def test_gates_of_selections_that_nobody_lists_do_not_count(N):
+    import mixture_experts_rank_b200 as more
+    args, _ = make(N, 72, 24, 16, 3)
+    args = masked(args, [0, 1, 2, 7])  # token 0 keeps nothing, token 2 loses one
+    args["gate"].view(-1)[[0, 7]] = float("nan")
+    args["gate"].view(-1)[1] = float("inf")
+    out = more.experts(**args)
+    assert ok() and (out[0] == 0).all()
+    ref.check(out, *ref.forward(**args), "out")
+
+
+@pytest.mark.parametrize("N", [3, 200])
+def test_an_infinite_middle_gives_infinity(N):
+    import mixture_experts_rank_b200 as more
+    args, _ = make(N, 64, 16, 1, 1)
+    args["X"].fill_(1.0)
+    args["W_up"].fill_(1e20)
+    args["W_down"].fill_(0.5)
+    out = more.experts(**args)
+    assert ok() and (out == float("inf")).all()
 
 
 def every_call(seed=0):
