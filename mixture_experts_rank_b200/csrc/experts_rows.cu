@@ -135,29 +135,43 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 }
 
 // A thread takes 8 columns of a token (and those `across` threads further on); `across`, a power of two, threads a
-// token.  Four rows' loads are in flight a thread, and the small register count keeps every thread slot of the SM busy:
-// that, not the loads a thread, is what reaches the memory's bandwidth here.
-__global__ void __launch_bounds__(256)
+// token; `each` tokens one after the other.  Bound by DRAM: every slot's row is read once.  Four rows' loads are in flight
+// a thread, and the rows that come next are looked up meanwhile; looked up when they are needed, they take as long as the
+// loads themselves (N = 262144, h = 512, k = 4: 282 us; so: 203 us, the rate of a plain copy).
+__device__ __forceinline__ void rows_of(const int32_t* __restrict__ slot_row, int64_t n, int j0, int k, int (&r)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = j0 + j < k ? __ldg(slot_row + n * k + j0 + j) : -1;
+}
+
+__global__ void __launch_bounds__(256, 5)
     combine_kernel(const __nv_bfloat16* __restrict__ y, const int32_t* __restrict__ slot_row, int64_t N, int h, int k,
-                   int log_across, __nv_bfloat16* __restrict__ out) {
+                   int log_across, int each, __nv_bfloat16* __restrict__ out) {
   after_previous();
-  const int groups = h >> 3, across = 1 << log_across;
-  const int64_t n = (int64_t)blockIdx.x * (256 >> log_across) + (threadIdx.x >> log_across);
-  if (n >= N) return;
-  const int32_t* rows = slot_row + n * k;
-  for (int c = threadIdx.x & (across - 1); c < groups; c += across) {
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int j0 = 0; j0 < k; j0 += 4) {
-      uint4 v[4];
+  const int groups = h >> 3, across = 1 << log_across, tokens = 256 >> log_across;
+  int64_t n = (int64_t)blockIdx.x * each * tokens + (threadIdx.x >> log_across);
+  const int64_t end = min(N, (int64_t)(blockIdx.x + 1) * each * tokens);
+  const int c0 = threadIdx.x & (across - 1);
+  if (n >= end || c0 >= groups) return;
+  int r[4], next[4];
+  rows_of(slot_row, n, 0, k, r);
+  for (; n < end; n += tokens) {
+    for (int c = c0; c < groups; c += across) {
+      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int j0 = 0; j0 < k; j0 += 4) {
+        uint4 v[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = j0 + j < k ? __ldg(rows + j0 + j) : -1;
-        v[j] = row >= 0 ? __ldcs(reinterpret_cast<const uint4*>(y + (size_t)row * h) + c) : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < 4; ++j)
+          v[j] = r[j] >= 0 ? __ldcs(reinterpret_cast<const uint4*>(y + (size_t)r[j] * h) + c) : make_uint4(0, 0, 0, 0);
+        const bool more = j0 + 4 < k, same = more || c + across < groups;
+        const int64_t at = same ? n : n + tokens;
+        if (at < end) rows_of(slot_row, at, more ? j0 + 4 : 0, k, next);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) add8(acc, v[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = next[j];
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) add8(acc, v[j]);
+      reinterpret_cast<uint4*>(out + (size_t)n * h)[c] = pack8(acc);
     }
-    reinterpret_cast<uint4*>(out + (size_t)n * h)[c] = pack8(acc);
   }
 }
 
@@ -348,9 +362,10 @@ cudaError_t launch_combine(const ExpertsArgs& a, const Rows& r, const __nv_bfloa
       log_across = l;
     }
   }
-  const int tokens = 256 >> log_across;
-  return launch_next(combine_kernel, dim3((unsigned)((a.N + tokens - 1) / tokens)), dim3(256), 0, a.stream, 1, y,
-                     r.slot_row, a.N, a.h, a.k, log_across, static_cast<__nv_bfloat16*>(out));
+  const int64_t tokens = 256 >> log_across, blocks = (a.N + tokens - 1) / tokens;
+  const int each = blocks >= 8192 ? 4 : 1;  // several tokens a thread where the SMs (5 blocks each) still get many blocks
+  return launch_next(combine_kernel, dim3((unsigned)((blocks + each - 1) / each)), dim3(256), 0, a.stream, 1, y, r.slot_row,
+                     a.N, a.h, a.k, log_across, each, static_cast<__nv_bfloat16*>(out));
 }
 
 cudaError_t launch_gate_grads(const ExpertsArgs& a, const Rows& r, const float* part, int parts, int64_t R) {

@@ -83,6 +83,21 @@ def test_experts(size, how):
     ref.check(out, *ref.forward(**args), "out")
 
 
+@pytest.mark.parametrize("size", [(66001, 16, 8, 8, 5), (66000, 16, 8, 16, 1), (33001, 264, 8, 8, 2)], ids=str)
+def test_many_tokens_of_short_rows(size):
+    """Enough tokens that a thread sums several of them, a last block that is not full, tokens that keep nothing."""
+    import mixture_experts_rank_b200 as more
+    args, out_bar = make(*size)
+    args = masked(args, [0, size[0] * size[4] // 2, size[0] * size[4] - 1])
+    out, untouched = guarded((size[0], size[1]), torch.bfloat16)
+    more.experts(**args, out=out)
+    x_bar = more.experts_backward(**args, out_bar=out_bar)[0]
+    assert ok() and untouched()
+    ref.check(out, *ref.forward(**args), "out")
+    want, bound = ref.backward(**args, out_bar=out_bar)
+    ref.check(x_bar, want["X_bar"], bound["X_bar"], "X_bar")
+
+
 @pytest.mark.parametrize("rows,width", [(1, 16), (3, 48), (130, 2048), (7, 4112)])
 def test_quantize_rows_is_exact(rows, width):
     import mixture_experts_rank_b200 as more
