@@ -235,17 +235,9 @@ __device__ __forceinline__ float top8(uint4 w, float top) {
 
 __device__ __forceinline__ uint2 round8x8(uint4 w, float div, float inv) {
   const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&w);
-  union {
-    int8_t b[8];
-    uint2 u;
-  } o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __bfloat1622float2(p[i]);
-    o.b[2 * i] = round8(f.x, div, inv);
-    o.b[2 * i + 1] = round8(f.y, div, inv);
-  }
-  return o.u;
+  const float2 a = __bfloat1622float2(p[0]), b = __bfloat1622float2(p[1]), c = __bfloat1622float2(p[2]),
+               d = __bfloat1622float2(p[3]);
+  return make_uint2(round8x4(a.x, a.y, b.x, b.y, div, inv), round8x4(c.x, c.y, d.x, d.y, div, inv));
 }
 
 // One warp per row (width a multiple of 16): no barrier, and enough rows in flight to cover the latency of one.  The
@@ -313,15 +305,8 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     const float div = top > 0.f ? top : 1.f, inv = __fdiv_rn(127.f, div);
-    auto round4 = [&](float4 f) {
-      char4 o;
-      o.x = round8(f.x, div, inv);
-      o.y = round8(f.y, div, inv);
-      o.z = round8(f.z, div, inv);
-      o.w = round8(f.w, div, inv);
-      return o;
-    };
-    char4* dst = reinterpret_cast<char4*>(q + row * width);
+    auto round4 = [&](float4 f) { return round8x4(f.x, f.y, f.z, f.w, div, inv); };
+    uint32_t* dst = reinterpret_cast<uint32_t*>(q + row * width);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int c = lane + 32 * j;

@@ -678,10 +678,9 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
           uint32_t o[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            o[q] = 0;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              o[q] |= (uint32_t)(uint8_t)round8(__uint_as_float(va[i + 4 * q + r]), div, inv) << (8 * r);
+            const uint32_t* m = va + i + 4 * q;
+            o[q] = round8x4(__uint_as_float(m[0]), __uint_as_float(m[1]), __uint_as_float(m[2]), __uint_as_float(m[3]), div,
+                            inv);
           }
           *reinterpret_cast<uint4*>(static_cast<int8_t*>(p.out) + (size_t)row * p.s + hh * 32 + i) =
               make_uint4(o[0], o[1], o[2], o[3]);

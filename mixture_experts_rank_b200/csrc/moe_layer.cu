@@ -210,10 +210,8 @@ __device__ void round_tokens(const LayerArgs& a, float* warp_tops) {
     const float div = top > 0.f ? top : 1.f, inv = __fdiv_rn(127.f, div);
     for (int c = threadIdx.x; c < a.h / 8; c += kThreads) {
       widen8(src[c], x);
-      uint32_t o[2] = {0, 0};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i >> 2] |= (uint32_t)(uint8_t)round8(x[i], div, inv) << (8 * (i & 3));
-      reinterpret_cast<uint2*>(a.Xq + (size_t)n * a.h)[c] = make_uint2(o[0], o[1]);
+      reinterpret_cast<uint2*>(a.Xq + (size_t)n * a.h)[c] =
+          make_uint2(round8x4(x[0], x[1], x[2], x[3], div, inv), round8x4(x[4], x[5], x[6], x[7], div, inv));
     }
     if (threadIdx.x == 0) a.x_scale[n] = __fdiv_rn(top, 127.f);
     __syncthreads();
@@ -776,12 +774,7 @@ __device__ void round_middles(const LayerArgs& a, const Shared& sh, float* warp_
     const float div = top > 0.f ? top : 1.f, inv = __fdiv_rn(127.f, div);
     for (int c = threadIdx.x; c < a.s / 4; c += kThreads) {
       const float4 f = src[c];
-      char4 o;
-      o.x = round8(f.x, div, inv);
-      o.y = round8(f.y, div, inv);
-      o.z = round8(f.z, div, inv);
-      o.w = round8(f.w, div, inv);
-      reinterpret_cast<char4*>(a.mid_q + (size_t)i * a.s)[c] = o;
+      reinterpret_cast<uint32_t*>(a.mid_q + (size_t)i * a.s)[c] = round8x4(f.x, f.y, f.z, f.w, div, inv);
     }
     if (threadIdx.x == 0) a.mid_scale[i] = __fdiv_rn(top, 127.f);
     __syncthreads();
