@@ -346,9 +346,8 @@ more_status more_experts(const void* X, const void* W_up, const void* W_down, in
 
 /*
  * Rows in 8 bits, symmetric: with t the largest magnitude of a row, out_q = round(127 v / t) (halves to even) and
- * out_scale = t / 127; a row of zeros has scale 0.  V: bf16 [rows][width], finite, magnitudes up to 2^120; width a
- * multiple of 16.  For the weights of more_experts_int8 take their rows as they lie: M 2 s rows of width h, and M h
- * rows of width s.
+ * out_scale = t / 127; a row of zeros has scale 0.  V: bf16 [rows][width], finite; width a multiple of 16.  For the
+ * weights of more_experts_int8 take their rows as they lie: M 2 s rows of width h, and M h rows of width s.
  */
 more_status more_quantize_rows(const void* V, int64_t rows, int width, int8_t* out_q, float* out_scale, void* stream);
 

@@ -95,7 +95,8 @@ inline Rows carve_rows(Carver& c, int64_t S, int M) {
 // exact for a bf16 v, so the division would round no value across a half; the product with inv is off by less than
 // 127 * 3 * 2^-24 < 2.3e-5, and where one of the four comes that close to a half, all are divided.  Adding 1.5 * 2^23
 // rounds to a whole number in the mantissa's low bits: the conversion instructions run at an eighth of the rate.  Where top
-// is below 127 / FLT_MAX, inv is infinite and the product no number: those are divided too.  Rounding is bound by its
+// is below 127 / FLT_MAX, inv is infinite and the product no number: those are divided too.  From 2^121 on 127 v is beyond
+// the largest float, so of large rows the division takes 2^-8 of both sides.  Rounding is bound by its
 // instructions, so it branches once for four values (33.5 million of them in quantize_rows_kernel: 30 us, 36 us with a
 // branch a value; in quantize_bf16_kernel: 25 and 33 us).
 __device__ __forceinline__ uint32_t round8x4(float v0, float v1, float v2, float v3, float top, float inv) {
@@ -110,8 +111,9 @@ __device__ __forceinline__ uint32_t round8x4(float v0, float v1, float v2, float
     near |= !(fabsf(y - (t[i] - kRound)) <= 0.5f - 4e-5f);
   }
   if (near) {
+    const float part = top > 0x1p100f ? 0x1p-8f : 1.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) t[i] = __fdiv_rn(127.f * v[i], top) + kRound;
+    for (int i = 0; i < 4; ++i) t[i] = __fdiv_rn(127.f * part * v[i], part * top) + kRound;
   }
   const uint32_t lo = __byte_perm(__float_as_uint(t[0]), __float_as_uint(t[1]), 0x0040);
   const uint32_t hi = __byte_perm(__float_as_uint(t[2]), __float_as_uint(t[3]), 0x0040);
