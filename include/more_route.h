@@ -346,15 +346,17 @@ more_status more_experts(const void* X, const void* W_up, const void* W_down, in
 
 /*
  * Rows in 8 bits, symmetric: with t the largest magnitude of a row, out_q = round(127 v / t) (halves to even) and
- * out_scale = t / 127; a row of zeros has scale 0.  V: bf16 [rows][width], finite; width a multiple of 16.  For the
- * weights of more_experts_int8 take their rows as they lie: M 2 s rows of width h, and M h rows of width s.
+ * out_scale = t / 127; a row of zeros has scale 0.  A row with an infinity has scale infinity, out_q = 127 or -127 at
+ * its infinities and 0 elsewhere; a row with a NaN has scale NaN and out_q = 0.  V: bf16 [rows][width]; width a multiple
+ * of 16.  For the weights of more_experts_int8 take their rows as they lie: M 2 s rows of width h, and M h rows of width s.
  */
 more_status more_quantize_rows(const void* V, int64_t rows, int width, int8_t* out_q, float* out_scale, void* stream);
 
 /*
  * more_experts with 8-bit operands: W_up int8 [M][2 s][h] and W_down int8 [M][h][s] with a scale per output channel
  * (up_scale fp32 [M][2 s], down_scale fp32 [M][h]; as more_quantize_rows gives them), and x and silu(A x) * (B x)
- * rounded to 8 bits by the same rule, a scale per row, before each product.  Products are summed exactly in 32-bit
+ * rounded to 8 bits by the same rule, a scale per row, before each product: a token with an infinity or NaN gives
+ * infinities and NaN, as in more_experts, and other tokens do not notice.  Products are summed exactly in 32-bit
  * integers, everything between them is fp32.  h and s are multiples of 16; else as more_experts.
  */
 size_t more_experts_int8_scratch_bytes(int64_t N, int h, int s, int M, int k);

@@ -383,7 +383,8 @@ def experts(X: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tensor, gate: tor
 
 def quantize_rows(V: torch.Tensor, *, out_q=None, out_scale=None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """Rows of V (bf16 [..., width], width a multiple of 16) in 8 bits: ``(q int8 [..., width], scale fp32 [...])``
-    with ``q = round(127 v / max|v|)``, halves to even, and ``scale = max|v| / 127``.  The weights of
+    with ``q = round(127 v / max|v|)``, halves to even, and ``scale = max|v| / 127``.  A row with an infinity has scale
+    infinity, ``q`` +-127 at its infinities and 0 elsewhere; a row with a NaN has scale NaN and ``q`` 0.  The weights of
     :func:`experts_int8` are ``quantize_rows(W_up)`` and ``quantize_rows(W_down)``."""
     V = _as_bf16(V, "V")
     if V.dim() < 1:

@@ -91,13 +91,22 @@ inline Rows carve_rows(Carver& c, int64_t S, int M) {
   return r;
 }
 
+// The larger of a row's largest magnitude so far and |v|, NaN once one of them is: what is no number of a row stays in
+// its scale.  One instruction, as the maximum that skips a NaN.
+__device__ __forceinline__ float top_of(float top, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(top), "f"(fabsf(v)));
+  return r;
+}
+
 // round-half-even(127 v / top) of four values |v| <= top, with `inv` = 127 / top, as the four bytes of a word.  127 v is
 // exact for a bf16 v, so the division would round no value across a half; the product with inv is off by less than
 // 127 * 3 * 2^-24 < 2.3e-5, and where one of the four comes that close to a half, all are divided.  Adding 1.5 * 2^23
 // rounds to a whole number in the mantissa's low bits: the conversion instructions run at an eighth of the rate.  Where top
 // is below 127 / FLT_MAX, inv is infinite and the product no number: those are divided too.  From 2^121 on 127 v is beyond
-// the largest float, so of large rows the division takes 2^-8 of both sides.  Rounding is bound by its
-// instructions, so it branches once for four values (33.5 million of them in quantize_rows_kernel: 30 us, 36 us with a
+// the largest float, so of large rows the division takes 2^-8 of both sides.  With an infinite top infinities give
+// +-127 and the rest 0; with one that is no number all give 0.
+// The kernels around it branch once for four values (33.5 million of them in quantize_rows_kernel: 30 us, 36 us with a
 // branch a value; in quantize_bf16_kernel: 25 and 33 us).
 __device__ __forceinline__ uint32_t round8x4(float v0, float v1, float v2, float v3, float top, float inv) {
   constexpr float kRound = 12582912.f;
@@ -113,12 +122,19 @@ __device__ __forceinline__ uint32_t round8x4(float v0, float v1, float v2, float
   if (near) {
     const float part = top > 0x1p100f ? 0x1p-8f : 1.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) t[i] = __fdiv_rn(127.f * part * v[i], part * top) + kRound;
+    for (int i = 0; i < 4; ++i) {
+      float y = __fdiv_rn(127.f * part * v[i], part * top);
+      if (y != y) y = top == top ? copysignf(127.f, v[i]) : 0.f;
+      t[i] = y + kRound;
+    }
   }
   const uint32_t lo = __byte_perm(__float_as_uint(t[0]), __float_as_uint(t[1]), 0x0040);
   const uint32_t hi = __byte_perm(__float_as_uint(t[2]), __float_as_uint(t[3]), 0x0040);
   return __byte_perm(lo, hi, 0x5410);
 }
+
+// What a row's values are divided by: its largest magnitude, 1 for a row of zeros.
+__device__ __forceinline__ float divisor_of(float top) { return top == 0.f ? 1.f : top; }
 
 // A launch that the stream may prepare while the kernel before it ends: the kernel's first action on global memory is
 // after_previous(), which waits for everything before it.  A call of the experts is up to nine short kernels, and this
@@ -156,7 +172,7 @@ cudaError_t launch_combine(const ExpertsArgs& a, const Rows& r, const __nv_bfloa
 // gate_bar[slot] = the sum of `parts` partial sums [parts][R] in order, and the logits' gradient
 // of a softmax over the k gates.
 cudaError_t launch_gate_grads(const ExpertsArgs& a, const Rows& r, const float* part, int parts, int64_t R);
-// Symmetric 8-bit rounding of rows: scale = max |v| / 127, q = round-half-even(127 v / max |v|).
+// Symmetric 8-bit rounding of rows: scale = max |v| / 127 (NaN where a value is), q = round-half-even(127 v / max |v|).
 cudaError_t launch_quantize_bf16(const __nv_bfloat16* v, int64_t rows, int width, int8_t* q, float* scale,
                                  cudaStream_t stream);
 // The same for the rows that a call uses of an fp32 [R][width] buffer (every tile's slots).

@@ -223,14 +223,16 @@ __global__ void __launch_bounds__(256)
 
 constexpr int kHeld = 8;  // 16-byte pieces of a row that a lane keeps between the two passes
 
-__device__ __forceinline__ float top8(uint4 w, float top) {
-  const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&w);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __bfloat1622float2(p[i]);
-    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-  }
+// Largest magnitudes of bf16 pairs as their bits, whose order that of the magnitudes is, a NaN above all.
+__device__ __forceinline__ uint32_t top_pairs(uint32_t top, uint32_t w) {
+  asm("max.u16x2 %0, %0, %1;" : "+r"(top) : "r"(w));
   return top;
+}
+
+__device__ __forceinline__ uint32_t top8(uint4 w, uint32_t top) {
+  constexpr uint32_t kMagnitude = 0x7fff7fffu;
+  return top_pairs(top_pairs(top_pairs(top_pairs(top, w.x & kMagnitude), w.y & kMagnitude), w.z & kMagnitude),
+                   w.w & kMagnitude);
 }
 
 __device__ __forceinline__ uint2 round8x8(uint4 w, float div, float inv) {
@@ -257,13 +259,12 @@ __global__ void __launch_bounds__(128, 8)
     const int c = lane + i * 32;
     held[i] = c < n ? src[c] : make_uint4(0, 0, 0, 0);
   }
-  float top = 0.f;
+  uint32_t tops = 0;
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) top = top8(held[i], top);
-  for (int c = lane + kHeld * 32; c < n; c += 32) top = top8(src[c], top);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  const float div = top > 0.f ? top : 1.f, inv = __fdiv_rn(127.f, div);
+  for (int i = 0; i < kHeld; ++i) tops = top8(held[i], tops);
+  for (int c = lane + kHeld * 32; c < n; c += 32) tops = top8(src[c], tops);
+  const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, max(tops << 16, tops & 0xffff0000u)));
+  const float div = divisor_of(top), inv = __fdiv_rn(127.f, div);
   uint2* dst = reinterpret_cast<uint2*>(q + row * width);
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
@@ -296,15 +297,15 @@ __global__ void __launch_bounds__(256)
       held[j] = c < n ? src[c] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     auto top4 = [](float4 f, float top) {
-      return fmaxf(fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f.z), fabsf(f.w)));
+      return top_of(top_of(top_of(top_of(top, f.x), f.y), f.z), f.w);
     };
     float top = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) top = top4(held[j], top);
     for (int c = lane + 256; c < n; c += 32) top = top4(src[c], top);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float div = top > 0.f ? top : 1.f, inv = __fdiv_rn(127.f, div);
+    for (int d = 16; d > 0; d >>= 1) top = top_of(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float div = divisor_of(top), inv = __fdiv_rn(127.f, div);
     auto round4 = [&](float4 f) { return round8x4(f.x, f.y, f.z, f.w, div, inv); };
     uint32_t* dst = reinterpret_cast<uint32_t*>(q + row * width);
 #pragma unroll

@@ -664,14 +664,14 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
         const float u = __uint_as_float(vb[i]) * (row_factor * scale_at(scales + HALF / 2 * 4, i, sb));
         const float m = a * sigmoid(a) * u;
         va[i] = __float_as_uint(m);
-        if (i < width) top = fmaxf(top, fabsf(m));
+        if (i < width) top = top_of(top, m);
       }
       st_shared_f32(tops + (parity * 256 + hh * 128 + t) * 4, top);
       asm volatile("bar.sync %0, 64;" ::"r"(1 + sp) : "memory");
-      top = fmaxf(top, ld_shared_f32(tops + (parity * 256 + (hh ^ 1) * 128 + t) * 4));
+      top = top_of(top, ld_shared_f32(tops + (parity * 256 + (hh ^ 1) * 128 + t) * 4));
       parity ^= 1;
       if (t < k.n) {
-        const float div = top > 0.f ? top : 1.f, inv = __fdiv_rn(127.f, div);
+        const float div = divisor_of(top), inv = __fdiv_rn(127.f, div);
 #pragma unroll
         for (int i = 0; i < 32; i += 16) {
           if (i >= width) break;

@@ -187,12 +187,12 @@ __device__ void project_tokens(const LayerArgs& a, float (*part)[16]) {
 
 // The largest of a CTA's values.
 __device__ __forceinline__ float block_max(float v, float* warp_tops) {
-  // the float order of magnitudes is their bits' order
+  // the float order of magnitudes is their bits' order, a NaN above all
   v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
   if ((threadIdx.x & 31) == 0) warp_tops[threadIdx.x >> 5] = v;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) v = fmaxf(v, warp_tops[w]);
+  for (int w = 0; w < kWarps; ++w) v = top_of(v, warp_tops[w]);
   return v;
 }
 
@@ -204,10 +204,10 @@ __device__ void round_tokens(const LayerArgs& a, float* warp_tops) {
     for (int c = threadIdx.x; c < a.h / 8; c += kThreads) {
       widen8(src[c], x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+      for (int i = 0; i < 8; ++i) top = top_of(top, x[i]);
     }
     top = block_max(top, warp_tops);
-    const float div = top > 0.f ? top : 1.f, inv = __fdiv_rn(127.f, div);
+    const float div = divisor_of(top), inv = __fdiv_rn(127.f, div);
     for (int c = threadIdx.x; c < a.h / 8; c += kThreads) {
       widen8(src[c], x);
       reinterpret_cast<uint2*>(a.Xq + (size_t)n * a.h)[c] =
@@ -768,10 +768,10 @@ __device__ void round_middles(const LayerArgs& a, const Shared& sh, float* warp_
     float top = 0.f;
     for (int c = threadIdx.x; c < a.s / 4; c += kThreads) {
       const float4 f = src[c];
-      top = fmaxf(fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f.z), fabsf(f.w)));
+      top = top_of(top_of(top_of(top_of(top, f.x), f.y), f.z), f.w);
     }
     top = block_max(top, warp_tops);
-    const float div = top > 0.f ? top : 1.f, inv = __fdiv_rn(127.f, div);
+    const float div = divisor_of(top), inv = __fdiv_rn(127.f, div);
     for (int c = threadIdx.x; c < a.s / 4; c += kThreads) {
       const float4 f = src[c];
       reinterpret_cast<uint32_t*>(a.mid_q + (size_t)i * a.s)[c] = round8x4(f.x, f.y, f.z, f.w, div, inv);
