@@ -327,8 +327,8 @@ more_status more_route_backward(const void* X, const void* R1, const void* R2, i
  *   offsets  int32 [M + 1], slots int32 [N k]   as more_dispatch writes them; a slot is listed at most once
  *   out      bf16 [N][h]        overwritten; a token none of whose slots is listed gets zeros
  * Both products are accumulated in fp32; silu(A x) * (B x) and each slot's row of the second product, already
- * times its gate, are rounded to bf16, and a token's k rows are summed in fp32 in the order of j.  Up to 16
- * tokens, or 64 with N k <= M (and M <= 16384), run in the one kernel of more_moe_layer, which carries the former as a
+ * times its gate, are rounded to bf16, and a token's k rows are summed in fp32 in the order of j.  Up to 16 tokens, or 64
+ * with N k <= M and N k h <= 2^21 (and M <= 16384), run in the one kernel of more_moe_layer, which carries the former as a
  * bf16 pair (about 16 bits) and the latter in fp32.  The result does not depend on the launch.
  * Offsets that fall or lie outside [0, N k] give zeros, and a slot outside [0, N k) is skipped; both set
  * MORE_DEVERR_BAD_INPUT.
@@ -388,10 +388,10 @@ more_status more_experts_backward(const void* X, const void* W_up, const void* W
 
 /*
  * The whole MoE layer (MoRE §2 "MoE layer"): more_route and then the selected experts, out = the `out` of more_experts
- * for the router's own selections and gates.  For a few tokens (N <= 64, decoding) everything runs in one kernel that
- * reads each selected expert's weights once; its logits are more_route's up to the order of their sums, and
- * silu(A x) * (B x) is carried as a bf16 pair (about 16 bits) and the slots' rows in fp32.  For more the call runs
- * more_route, more_dispatch and more_experts.
+ * for the router's own selections and gates.  Up to 64 tokens (decoding), of any h, everything runs in one kernel that
+ * reads each selected expert's weights once for every 8 of its selections; its logits are more_route's up to the order
+ * of their sums, and silu(A x) * (B x) is carried as a bf16 pair (about 16 bits) and the slots' rows in fp32.  For more
+ * the call runs more_route, more_dispatch and more_experts.
  * Arguments and requirements: those of more_route (X, R1, R2, r, k, M) and of more_experts (W_up, W_down, s, out).
  * scratch: at least more_moe_layer_scratch_bytes(N, h, s, M, k) bytes, 16-byte aligned, one for each call that may
  * overlap.  Asynchronous on `stream`; allocates nothing; may be captured into a graph.  The few-token kernel is a

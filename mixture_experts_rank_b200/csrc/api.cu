@@ -524,7 +524,7 @@ LayerBuffers carve_layer(void* scratch, int64_t N, int h, int s, int M, int k, b
   const int64_t S = N * k;
   b.idx = c.take<int32_t>(S);
   b.gate = c.take<float>(S);
-  if (layer_few_fits(N, h, k)) {
+  if (layer_few_fits(N)) {
     b.barrier = c.take<unsigned int>(1);
     b.z = c.take<float>(N * 128);  // r <= 128
     b.logits = c.take<float>(N * M);
@@ -563,7 +563,7 @@ more_status moe_layer(const void* X, const void* R1, const void* R2, const void*
   if (scratch_bytes < b.bytes) return MORE_ERR_INVALID_ARG;
   unsigned int* status = status_word();
   if (!status) return MORE_ERR_CUDA;
-  if (!layer_few_fits(N, h, k)) {
+  if (!layer_few_fits(N)) {
     more_status st = more_route(X, R1, R2, N, h, r, M, k, b.idx, b.gate, b.counts, nullptr, stream);
     if (st == MORE_OK)
       st = more_dispatch(b.idx, N, k, M, b.offsets, b.slots, b.dispatch, b.dispatch_bytes, stream);

@@ -202,7 +202,7 @@ struct FewArgs {
   unsigned int* status;
   cudaStream_t stream;
 };
-bool layer_few_fits(int64_t N, int h, int k);
+bool layer_few_fits(int64_t N);
 // The same kernel for selections that were dispatched before.
 bool experts_few_fits(int64_t N, int h, int M, int k);
 cudaError_t launch_layer_few(const FewArgs& f);

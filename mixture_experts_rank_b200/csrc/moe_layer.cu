@@ -11,7 +11,8 @@
 //      Where there are too few rows for the machine's warps, 2 to 16 warps of a CTA share them, each a part of h.
 //   5. Down: every CTA owns h / CTAs output channels for all experts, so a token's k contributions meet in its
 //      shared memory, and out[n] = sum_j gate * y is summed there in the order of j: no second pass over a row buffer,
-//      and no atomics on the result.
+//      and no atomics on the result.  Where all N k selections of these channels are more than it holds (N = 64, k = 8:
+//      from h = 5477 on), the CTA takes its channels in runs, one after the other.
 //
 // The products of 4 and 5 are warp MMAs (m16n8k16; k32 for 8 bits) with the weights as the 16 rows of A and a group's
 // up to 8 tokens as the columns of B.  The tensor cores are not what a few rows an expert need; their operand layout is:
@@ -40,11 +41,12 @@ constexpr int kGroup = 8;  // selections of one expert that share a reading of i
 constexpr int kRows = 16;  // rows of an MMA
 constexpr int64_t kFewTokens = 64;
 constexpr int64_t kFewRows = 16;  // tokens up to which the experts alone run here whatever they share
+constexpr int64_t kFewSums = 1 << 21;  // N k h up to which more than those do
 constexpr int kFewExperts = 16384;  // every CTA reads all the offsets of a dispatch
 constexpr int kSolo = 2;         // tokens that every CTA routes for itself
 constexpr int kSlots = 4;                   // batches of a warp's ring
 constexpr uint32_t kRing = 128 * 1024;      // all warps' rings
-constexpr uint32_t kSmemMost = 200 * 1024;  // dynamic
+constexpr uint32_t kSmemMost = 218 * 1024;  // dynamic: 227 KB less the kernel's static 8.1
 constexpr int kCandidates = 512;  // as many as threads: where there is no bound there may be that many logits
 
 struct LayerArgs {
@@ -78,12 +80,12 @@ struct Shared {
   int32_t* group_e;    // [S] expert of a group
   int32_t* group_n;    // [S] its selections
   int16_t* member;     // [S][kGroup] selections of a group
-  float* y;            // [S][R]
+  float* y;            // [S][R], R channels of a CTA at a time
 };
 
-__host__ __device__ inline uint32_t round16(uint32_t v) { return (v + 15) & ~15u; }
+__host__ __device__ constexpr uint32_t round16(uint32_t v) { return (v + 15) & ~15u; }
 
-__host__ __device__ inline uint32_t layer_smem(int S, int R) {
+__host__ __device__ constexpr uint32_t layer_smem(int S, int R) {
   return kRing + round16(4 * S) * 4 + round16(2 * kGroup * S) + round16(4 * S * R);
 }
 
@@ -781,35 +783,28 @@ __device__ void round_middles(const LayerArgs& a, const Shared& sh, float* warp_
   }
 }
 
-// Step 5.  Unit u: rows 16 (u % tiles) on of this CTA's for group u / tiles.  The first batches' copies start before
-// the barrier: they need the groups alone.
+// Step 5 for a run of this CTA's channels.  Unit u: rows 16 (u % tiles) on of the run for group u / tiles.  The first
+// batches' copies start before the barrier: they need the groups alone.
 template <bool I8, int BS>
 struct Down {
   using R = Ring<BS>;
   static constexpr int kBytes = I8 ? 1 : 2;
   const LayerArgs& a;
   const Shared& sh;
-  int o0, rows, tiles, units, batches, pitch, lane, warp, pc, r0;
+  int groups, o0, rows, tiles, units, batches, pitch, lane, warp, pc, r0;
   R ring;
   int fu, fb, left = 0;
   const uint8_t* from;
 
   __device__ __forceinline__ int group_of(int u) const { return tiles == 1 ? u : u / tiles; }
-  __device__ Down(const LayerArgs& a_, const Shared& sh_, int groups, int rows_each) : a(a_), sh(sh_) {
+  __device__ Down(const LayerArgs& a_, const Shared& sh_, int groups_) : a(a_), sh(sh_), groups(groups_) {
     warp = threadIdx.x >> 5;
     lane = threadIdx.x & 31;
-    o0 = blockIdx.x * rows_each;
-    rows = max(0, min(rows_each, a.h - o0));
-    tiles = (rows + kRows - 1) / kRows;
-    units = warp < R::kStreams ? groups * tiles : 0;
     pitch = a.s * kBytes;
     batches = (pitch + (int)R::kBatch - 1) / (int)R::kBatch;
     pc = lane % R::kPieces;
     r0 = lane / R::kPieces;
     ring.base = sh.ring + (uint32_t)warp * R::kBytes;
-    fu = warp;
-    fb = 0;
-    locate();
   }
   __device__ __forceinline__ void locate() {
     if (fu >= units) return;
@@ -835,7 +830,16 @@ struct Down {
     }
     R::commit();
   }
-  __device__ void start() {
+  // The channels [from_row, to_row); whatever was copied for the last ones has been used.
+  __device__ void start(int from_row, int to_row) {
+    o0 = from_row;
+    rows = max(0, to_row - from_row);
+    tiles = (rows + kRows - 1) / kRows;
+    units = warp < R::kStreams ? groups * tiles : 0;
+    ring.in = ring.out = 0;
+    fu = warp;
+    fb = 0;
+    locate();
     if (warp < R::kStreams) {
 #pragma unroll 1
       for (int i = 0; i < kSlots - 1; ++i) fetch();
@@ -923,20 +927,32 @@ struct Down {
   }
 };
 
+// `rows_each` channels a CTA, `rows_once` of them at a time.
 template <bool I8, int BS>
 __device__ __forceinline__ void down_phase(const LayerArgs& a, const Shared& sh, int groups, int rows_each,
-                                           unsigned turn, int* failed) {
+                                           int rows_once, unsigned turn, int* failed) {
   __syncthreads();  // other warps' rings of the first product lie in this one's
-  Down<I8, BS> down(a, sh, groups, rows_each);
-  down.start();
-  if (grid_barrier(a.barrier, turn, a.status, failed))
-    down.run();
-  else
+  int row = (int)blockIdx.x * rows_each;
+  const int end = min(a.h, row + rows_each);
+  Down<I8, BS> down(a, sh, groups);
+  down.start(row, min(end, row + rows_once));
+  if (!grid_barrier(a.barrier, turn, a.status, failed)) {
     asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
+  for (;;) {
+    down.run();
+    row += rows_once;
+    if (row >= end) break;
+    __syncthreads();  // sh.y has been summed
+    down.start(row, min(end, row + rows_once));
+    __syncthreads();  // and is zero
+  }
 }
 
 template <bool I8>
-__global__ void __launch_bounds__(kThreads, 1) layer_kernel(const __grid_constant__ LayerArgs a, int rows_each) {
+__global__ void __launch_bounds__(kThreads, 1) layer_kernel(const __grid_constant__ LayerArgs a, int rows_each,
+                                                              int rows_once) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ union {
     float part[kWarps][16];
@@ -971,9 +987,9 @@ __global__ void __launch_bounds__(kThreads, 1) layer_kernel(const __grid_constan
   }
   // rows of up to 128 bytes fill the ring in batches of two steps, longer ones in batches of four
   if (a.s * (I8 ? 1 : 2) <= 128)
-    down_phase<I8, 2>(a, sh, groups, rows_each, ++turn, &failed);
+    down_phase<I8, 2>(a, sh, groups, rows_each, rows_once, ++turn, &failed);
   else
-    down_phase<I8, 4>(a, sh, groups, rows_each, ++turn, &failed);
+    down_phase<I8, 4>(a, sh, groups, rows_each, rows_once, ++turn, &failed);
 }
 
 int sm_count() {
@@ -986,7 +1002,9 @@ int sm_count() {
 template <bool I8>
 cudaError_t launch_layer(const LayerArgs& a, cudaStream_t stream) {
   const int grid = sm_count();
-  const int rows_each = (a.h + grid - 1) / grid;
+  // a CTA's share of the channels, in as few runs as their sums' place allows: never less than 14 channels for 1024 selections
+  const int rows_each = (a.h + grid - 1) / grid, most = (int)((kSmemMost - layer_smem(a.S, 0)) / (4 * (uint32_t)a.S));
+  const int runs = (rows_each + most - 1) / most, rows_once = (rows_each + runs - 1) / runs;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -999,33 +1017,37 @@ cudaError_t launch_layer(const LayerArgs& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = layer_smem(a.S, rows_each);
+  cfg.dynamicSmemBytes = layer_smem(a.S, rows_once);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;  // every CTA waits for the others at the barriers
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, layer_kernel<I8>, a, rows_each);
+  return cudaLaunchKernelEx(&cfg, layer_kernel<I8>, a, rows_each, rows_once);
 }
 
 }  // namespace
 
-// The few-token kernel takes the shape: its shared memory holds the selections' output channels (a CTA's share of h,
-// at least 132 CTAs assumed), and a batch of up to kFewTokens tokens.  The layer gains by it up to there: it saves the
+// The few-token kernel takes up to kFewTokens tokens.  The layer gains by it up to there: it saves the
 // router's launches too (N = 64: h = 2048, s = 64, M = 4096, k = 8: 98 us against 139; 1024, 256, 128, 4: 67 against
-// 81; only weights of 0.8 GB, 2048, 1024, 64, 4, take 186 against 177).
+// 81; h = 4096, s = 64, M = 512, k = 8: 129 against 155; 7168, 64, 512, 8: 217 against 243, in 8 bits 200 against 247).
+// It keeps the sizes where reading more than about a GB of weights at 4 to 5 TB/s costs more than the launches (2048,
+// 1024, 64, 4: 186 against 177; 5120, 128, 512, 8: 293 against 249; 7168, 256, 256, 8: 497 against 430): what is rounded
+// then depends on neither h nor the experts' sizes.
 // The experts alone gain while the selections seldom share an expert, whose weights this kernel then reads at 4 TB/s in
 // one launch, and the grouped products at 5.8 after five launches.  us, few against grouped:
 //   2048, 64, 4096, 8:   N = 8: 25, 39    N = 64: 87, 94        2048, 1024, 64, 4:  N = 16: 107, 108    N = 32: 137, 122
 //   512, 64, 1024, 4:    N = 8: 18, 26    N = 64: 31, 30        1024, 256, 128, 4:  N = 32: 49, 48      N = 64: 59, 51
+//   4096, 64, 512, 8:    N = 40: 94, 104  N = 64: 117, 118      4096, 128, 512, 8:  N = 40: 170, 143    N = 64: 216, 174
+// Beyond N k h = kFewSums the sums would be taken in runs of channels, and they lose: 5120, 128, 512, 8, N = 64: 280, 211;
+// 7168, 256, 256, 4, N = 64: 347, 292 (and with narrow rows gain little: 7168, 64, 512, 8, N = 64: 203, 198).
 bool experts_few_fits(int64_t N, int h, int M, int k) {
-  return N > 0 && M <= kFewExperts && (N <= kFewRows || N * k <= M) && layer_few_fits(N, h, k);
+  return N > 0 && M <= kFewExperts && layer_few_fits(N) && (N <= kFewRows || (N * k <= M && N * k * h <= kFewSums));
 }
 
-bool layer_few_fits(int64_t N, int h, int k) {
-  return N <= kFewTokens && layer_smem((int)(N * k), (h + 131) / 132) <= kSmemMost;
-}
+bool layer_few_fits(int64_t N) { return N <= kFewTokens; }
+static_assert(kSmemMost >= layer_smem(kFewTokens * MORE_KMAX, 14), "room for a run of channels");
 
 cudaError_t launch_layer_few(const FewArgs& f) {
   LayerArgs a = {};

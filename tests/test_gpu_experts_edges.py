@@ -3,9 +3,11 @@ import pytest
 import torch
 
 from tests import experts_reference as ref
-from tests.test_gpu_experts import int8_of, layer_inputs, make, ok, rnd
+from tests.parity import FINE_TOL
+from tests.test_gpu_experts import guarded, int8_of, layer_inputs, layer_reference, make, ok, rnd
 
 pytestmark = pytest.mark.gpu
+
 
 def check(got, want, bound, name):
     """ref.check, and the expected values have to be numbers themselves."""
@@ -134,3 +136,78 @@ def test_layer_in_8_bits_of_a_token_that_is_no_number():
     assert more.device_status() != 0
     keep = torch.arange(9, device="cuda") != 4
     assert torch.equal(out[keep], clean[keep]) and (out[4] == 0).all()
+
+
+# ---- few tokens of any h ---------------------------------------------------------------------------------------------
+# N, h, r, s, M, k.  Sums of all selections of 64 tokens take one CTA's shared memory at k h of some 40000; the sizes lie
+# on both sides, up to several times it.  The bounds are those of a call that carries the rows in fp32 throughout.
+WIDE = [(64, 4096, 32, 16, 64, 8), (36, 7168, 32, 16, 64, 8), (37, 7168, 32, 16, 64, 8), (64, 7168, 32, 80, 64, 8),
+        (18, 7168, 16, 16, 64, 16), (64, 6000, 16, 16, 40, 16), (64, 20016, 16, 16, 24, 16), (2, 131072, 16, 16, 8, 2),
+        (64, 40000, 16, 16, 16, 2), (64, 2064, 16, 48, 16, 16)]
+
+
+def layer_check(out, args, k, **scales):
+    """The layer against the experts in 64 bits with more.route's gates.  The few-token kernel has a router of its own, and
+    each router's logits may be off by t = FINE_TOL of the token's rms (tests/parity.py; mostly z as a bf16 pair).  Logits
+    that differ by 2 t change a gate e^l_j / sum e^l_i by a factor of at most e^(4 t), so the result by as much of the
+    sum of its terms' magnitudes."""
+    import mixture_experts_rank_b200 as more
+    want, bound = layer_reference(args, k, True, **scales)
+    idx, gate, _, _ = more.route(args["X"], args["R1"], args["R2"], k)
+    offsets, slots = more.dispatch(idx, args["W_down"].shape[0])
+    terms = sum(ref.forward(args["X"], args["W_up"], args["W_down"], gate * one, offsets, slots, fp32_rows=True, **scales)[0].abs()
+                for one in torch.eye(k, device="cuda"))
+    rms = (args["X"].double() @ args["R1"].double() @ args["R2"].double()).square().mean(1, keepdim=True).sqrt()
+    check(out, want, bound + torch.expm1(4 * FINE_TOL * rms) * terms, "out")
+
+
+@pytest.mark.parametrize("size", WIDE, ids=str)
+def test_layer_of_wide_tokens(size):
+    import mixture_experts_rank_b200 as more
+    N, h, r, s, M, k = size
+    args = layer_inputs(N, h, r, s, M)
+    out, untouched = guarded((N, h), torch.bfloat16)
+    more.moe_layer(**args, k=k, out=out)
+    assert ok() and untouched()
+    layer_check(out, args, k)
+
+
+@pytest.mark.parametrize("size", WIDE, ids=str)
+def test_layer_of_wide_tokens_in_8_bits(size):
+    import mixture_experts_rank_b200 as more
+    N, h, r, s, M, k = size
+    args = int8_of(layer_inputs(N, h, r, s, M))
+    out, untouched = guarded((N, h), torch.bfloat16)
+    more.moe_layer_int8(**args, k=k, out=out)
+    assert ok() and untouched()
+    layer_check(out, args, k, **{n: args[n] for n in ("up_scale", "down_scale")})
+
+
+# N, h, s, M, k; up to 16 tokens of any h, and others with N k <= M up to N k h = 2^21: the third lies on it, the last
+# behind it, where each slot's row is rounded to bf16
+FEW = [(16, 30000, 16, 16, 16), (16, 7168, 48, 4, 4), (64, 4096, 16, 512, 8), (18, 7280, 32, 300, 16),
+       (64, 4112, 16, 512, 8)]
+
+
+@pytest.mark.parametrize("size", FEW, ids=str)
+def test_experts_of_few_wide_tokens(size):
+    import mixture_experts_rank_b200 as more
+    args, _ = make(*size)
+    fp32_rows = size != FEW[-1]
+    out, untouched = guarded(size[:2], torch.bfloat16)
+    more.experts(**args, out=out)
+    assert ok() and untouched()
+    check(out, *ref.forward(**args, fp32_rows=fp32_rows), "out")
+    args = int8_of(args)
+    more.experts_int8(**args, out=out)
+    assert ok() and untouched()
+    check(out, *ref.forward(**args, fp32_rows=fp32_rows), "out in 8 bits")
+
+
+def test_layer_in_8_bits_of_more_tokens_is_the_three_calls():
+    import mixture_experts_rank_b200 as more
+    a = int8_of(layer_inputs(130, 256, 32, 80, 32))
+    idx, gate, _, _ = more.route(a["X"], a["R1"], a["R2"], 4)
+    offsets, slots = more.dispatch(idx, 32)
+    want = more.experts_int8(a["X"], a["W_up"], a["up_scale"], a["W_down"], a["down_scale"], gate, offsets, slots)
+    assert torch.equal(more.moe_layer_int8(**a, k=4), want) and ok()
