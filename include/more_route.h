@@ -373,7 +373,9 @@ more_status more_experts_int8(const void* X, const int8_t* W_up, const float* up
  *   out_W_down_bar  bf16 [M][h][s]     the same
  *   out_gate_bar    fp32 [N][k]        dL/dgate
  *   out_logits_bar  fp32 [N][k]        dL/d(selected logits) = gate_j (gate_bar_j - sum_i gate_i gate_bar_i): the
- *                                      top_vals_bar of more_route_backward
+ *                                      top_vals_bar of more_route_backward.  A selection that no expert lists has
+ *                                      gate_bar_j = 0 and is not in the sum, whatever its gate; its own
+ *                                      logits_bar_j is -gate_j times the sum
  * Products are accumulated in fp32; the gradients of A x, B x and gate * silu(A x) * (B x), and each slot's row of the
  * X gradient, are rounded to bf16; the gates' gradients are fp32 throughout.  No atomics: the result does not depend
  * on the launch.  Other arguments and requirements as for more_experts, with

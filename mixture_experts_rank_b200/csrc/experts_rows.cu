@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Sixteen lanes a token, one a slot (k <= 16).
+// Sixteen lanes a token, one a slot (k <= 16).  The gate of a slot that no expert lists is in no sum: it may be no number.
 __global__ void __launch_bounds__(256)
     gate_grads_kernel(const float* __restrict__ part, int parts, int64_t R, const int32_t* __restrict__ slot_row,
                       const float* __restrict__ gate, int64_t N, int k, float* __restrict__ gate_bar,
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll 8
     for (int p = 0; p < parts; ++p) s += part[p * R + row];
   }
-  float dot = g * s;
+  float dot = row >= 0 ? g * s : 0.f;
 #pragma unroll
   for (int d = 8; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
   if (in) {

@@ -4,7 +4,7 @@ import torch
 
 from tests import experts_reference as ref
 from tests.parity import FINE_TOL
-from tests.test_gpu_experts import guarded, int8_of, layer_inputs, layer_reference, make, ok, rnd
+from tests.test_gpu_experts import guarded, int8_of, layer_inputs, layer_reference, make, masked, ok, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -211,3 +211,25 @@ def test_layer_in_8_bits_of_more_tokens_is_the_three_calls():
     offsets, slots = more.dispatch(idx, 32)
     want = more.experts_int8(a["X"], a["W_up"], a["up_scale"], a["W_down"], a["down_scale"], gate, offsets, slots)
     assert torch.equal(more.moe_layer_int8(**a, k=4), want) and ok()
+
+
+# ---- what counts for nothing -------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("size", [(9, 72, 24, 16, 3), (300, 72, 24, 16, 3), (600, 320, 712, 3, 2)], ids=str)
+def test_backward_with_gates_of_selections_that_nobody_lists(size):
+    import mixture_experts_rank_b200 as more
+    N, k = size[0], size[4]
+    args, d = make(*size)
+    drop = list(range(k)) + [2 * k + 1]  # token 0 keeps nothing, token 2 loses one
+    args = masked(args, drop)
+    gate = args["gate"].clone()
+    gate.view(-1)[drop] = 0.0  # what such a gate comes to
+    args["gate"].view(-1)[drop] = torch.tensor([NAN, INF, -INF, NAN], device="cuda")[-len(drop):]
+    got = more.experts_backward(**args, out_bar=d)
+    assert ok()
+    want, bound = ref.backward(**dict(args, gate=gate), out_bar=d)
+    for name, t in zip(want, got):
+        if name == "logits_bar":  # a selection that is not listed has its own gate as a factor
+            listed = torch.ones(N * k, dtype=torch.bool, device="cuda")
+            listed[drop] = False
+            t, want[name], bound[name] = (v.reshape(-1)[listed] for v in (t, want[name], bound[name]))
+        check(t, want[name], bound[name], name)
