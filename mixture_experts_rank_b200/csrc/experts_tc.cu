@@ -73,7 +73,7 @@ struct Shape {
   static constexpr uint32_t kOffScale = kOffOut + (kStaged ? kEpiWarps * kStageOut : 0);
   static constexpr uint32_t kOffTop = kOffScale + (kEight ? kEpiWarps * kScales * 4 : 0);
   static constexpr uint32_t kOffBar = kOffTop + (MODE == kUp8 ? 2 * 256 * 4 : 0);
-  static constexpr uint32_t kSmem = kOffBar + (2 * kMaxStages + 4 + 1) * 8 + 16 + 1024;
+  static constexpr uint32_t kSmem = kOffBar + (2 * kMaxStages + 4 + 1 + 4) * 8 + 16 + 1024;
 };
 
 struct Params {
@@ -98,6 +98,7 @@ struct Params {
 
 struct Bars {
   uint64_t *full, *empty, *acc_full, *acc_empty, *drain;
+  uint64_t* halves;  // [4] the two epilogue warps of a lane group
   uint32_t* tmem_slot;
   int* abort_flag;
 };
@@ -110,7 +111,8 @@ __device__ __forceinline__ Bars bars_at(uint8_t* p) {
   r.acc_full = b + 2 * kMaxStages;
   r.acc_empty = r.acc_full + 2;
   r.drain = r.acc_empty + 2;
-  r.tmem_slot = reinterpret_cast<uint32_t*>(r.drain + 1);
+  r.halves = r.drain + 1;
+  r.tmem_slot = reinterpret_cast<uint32_t*>(r.halves + 4);
   r.abort_flag = reinterpret_cast<int*>(r.tmem_slot + 1);
   return r;
 }
@@ -198,6 +200,14 @@ __device__ __forceinline__ bool poll_wait(uint64_t* bar, uint32_t parity, volati
   for (int i = 0; i < 4000; ++i)
     if (mbar_test_wait(bar, parity)) return true;
   return bounded_wait(bar, parity, abort_flag, status);
+}
+
+// A warp's wait: its lanes go on together or, once the wait has run out for one of them, give up together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Bars& b, unsigned int* status) {
+  return __all_sync(0xffffffffu, bounded_wait(bar, parity, b.abort_flag, status));
+}
+__device__ __forceinline__ bool warp_poll(uint64_t* bar, uint32_t parity, const Bars& b, unsigned int* status) {
+  return __all_sync(0xffffffffu, poll_wait(bar, parity, b.abort_flag, status));
 }
 
 template <class S>
@@ -631,7 +641,7 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
     }
     if (at.more()) info = row_info<MODE, HALF, PAIR>(p, PAIR ? part_of<S::kIsDw>(at.nxt, rank) : at.nxt, t, lane, hh);  // used a tile from now
     if (!empty && !S::kRuns) {
-      if (!bounded_wait(&b.acc_full[d.i], d.phase, b.abort_flag, p.status)) break;
+      if (!warp_wait(&b.acc_full[d.i], d.phase, b, p.status)) break;
       tc_fence_after();
     }
     const uint32_t acc = tmem + lanes + d.i * S::kAccStride;
@@ -667,7 +677,9 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
         if (i < width) top = top_of(top, m);
       }
       st_shared_f32(tops + (parity * 256 + hh * 128 + t) * 4, top);
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + sp) : "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.halves[sp]);  // not a named barrier: the other warp may have given up
+      if (!warp_poll(&b.halves[sp], parity, b, p.status)) break;
       top = top_of(top, ld_shared_f32(tops + (parity * 256 + (hh ^ 1) * 128 + t) * 4));
       parity ^= 1;
       if (t < k.n) {
@@ -744,7 +756,7 @@ __device__ void epilogue(const Params& p, const Bars& b, uint8_t* smem, uint32_t
         bool ok = true;
 #pragma unroll 1
         for (int r = 0; r < 2 * runs; ++r) {
-          if (!bounded_wait(&b.acc_full[d.i], d.phase, b.abort_flag, p.status)) {
+          if (!warp_wait(&b.acc_full[d.i], d.phase, b, p.status)) {
             ok = false;
             break;
           }
@@ -944,6 +956,7 @@ __global__ void __launch_bounds__(Shape<MODE, HALF, PAIR>::kThreads, 1)
       mbar_init(&b.acc_empty[i], PAIR ? 2 * kEpiWarps : kEpiWarps);
     }
     mbar_init(b.drain, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&b.halves[i], 2);
     *b.abort_flag = 0;
     fence_mbar_init();
   }
