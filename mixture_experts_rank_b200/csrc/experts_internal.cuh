@@ -3,8 +3,10 @@
 //
 // The slots sorted by expert (more_dispatch) are laid out as rows, each expert's rows starting at a
 // multiple of 16 (kRowPad: the K step of a 16-bit MMA, so that a product over an expert's rows can
-// end on a whole step).  A tile is up to 128 rows of one expert, 256 for CTA pairs.  Padding rows repeat
-// the expert's last token and carry slot -1.
+// end on a whole step).  A tile is up to 128 rows of one expert, 256 for CTA pairs.  Padding rows, and those of slots
+// out of range, carry slot -1.  A product over an expert's rows takes zeros for them, on both sides: a token's values could
+// be no numbers, and zero times those is none (backward of 32768 tokens: 339 us, 334 with a token's values).  The other
+// products may take any token's, the expert's last one's, since each row's results are its own.
 #pragma once
 #include "more_internal.cuh"
 
@@ -16,7 +18,7 @@ constexpr int kTileRows = 128;
 // Where a call's rows come from; all pointers are in the caller's scratch.
 struct Rows {
   int32_t* row_slot;   // [R] slot of a row, -1 for padding (and for a slot outside [0, S))
-  int32_t* row_token;  // [R] token of a row (any valid token where row_slot < 0)
+  int32_t* row_token;  // [R] token of a row; where row_slot < 0, -1 - t with any token t
   float* row_gate;     // [R] gate of a row's slot (0 where row_slot < 0)
   int32_t* slot_row;   // [S] row of a slot, -1 where no expert lists it
   int4* tiles;         // [T] {expert, first row, rows that are slots (at most the call's tile_rows), those padded}
@@ -77,6 +79,8 @@ struct Carver {
     return base ? p : nullptr;
   }
 };
+
+__device__ __forceinline__ int any_token(int row_token) { return row_token < 0 ? -1 - row_token : row_token; }
 
 inline Rows carve_rows(Carver& c, int64_t S, int M) {
   Rows r;

@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(2 * kTileRows)
   const int row = t.y + r;
   out.row_slot[row] = real ? slot : -1;
   const int token = ok ? slot / k : 0;
-  out.row_token[row] = token;
+  out.row_token[row] = real ? token : -1 - token;
   if (token_scale) row_scale[row] = token_scale[token];
   out.row_gate[row] = real ? gate[slot] : 0.f;
   if (real) out.slot_row[slot] = row;
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(256, 5)
   }
 }
 
-// One warp per row of the padded layout, eight pieces of 16 bytes in flight a lane.
+// One warp per row of the padded layout, eight pieces of 16 bytes in flight a lane; zeros for a row that is no slot.
 __global__ void __launch_bounds__(256)
     pick_kernel(const uint4* __restrict__ src, const int32_t* __restrict__ row_token, const int32_t* __restrict__ rows,
                 int pieces, uint4* __restrict__ dst) {
@@ -183,13 +183,14 @@ __global__ void __launch_bounds__(256)
   const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= *rows) return;
-  const uint4* from = src + (size_t)row_token[row] * pieces;
+  const int token = row_token[row];
+  const uint4* from = src + (size_t)max(token, 0) * pieces;
   uint4* to = dst + (size_t)row * pieces;
   for (int c = lane; c < pieces; c += 256) {
     uint4 v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c + 32 * i < pieces) v[i] = __ldg(from + c + 32 * i);
+      if (c + 32 * i < pieces) v[i] = token >= 0 ? __ldg(from + c + 32 * i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (c + 32 * i < pieces) to[c + 32 * i] = v[i];

@@ -361,11 +361,13 @@ __device__ void row_copies(const Params& p, const Bars& b, uint8_t* smem, int tu
           const int row = 4 * (turn + 4 * i) + sub;
           if (r0 + row >= k.padded) continue;
           const uint32_t dst = st + row * 128 + ((piece ^ (row & 7)) << 4);
+          const uint8_t* from = src + (size_t)max(tok[i], 0) * pitch;
+          const bool slot = tok[i] >= 0;
 #pragma unroll
           for (int x = 0; x < kBoxes; ++x) {
             const int cc = col + 64 * x + piece * 8;
             const bool ok = cc < p.h;
-            copy16(dst + x * kBox, src + (size_t)tok[i] * pitch + (ok ? 2 * cc : 0), ok);
+            copy16(dst + x * kBox, from + (ok ? 2 * cc : 0), ok && slot);
           }
         }
         arrive_landed(&b.full[c.pos.i]);
@@ -380,14 +382,14 @@ __device__ void row_copies(const Params& p, const Bars& b, uint8_t* smem, int tu
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int r = 4 * (turn + 4 * i) + sub;
-          tok[i] = r < k.padded ? p.rows.row_token[k.row + r] : 0;
+          tok[i] = r < k.padded ? any_token(p.rows.row_token[k.row + r]) : 0;
         }
       }
       int ahead[8];  // the next tile's tokens
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = 4 * (turn + 4 * i) + sub;
-        ahead[i] = at.more() && r < at.nxt.padded ? p.rows.row_token[at.nxt.row + r] : 0;
+        ahead[i] = at.more() && r < at.nxt.padded ? any_token(p.rows.row_token[at.nxt.row + r]) : 0;
         row[i] = X + tok[i] * pitch + piece * 16;
       }
       const int r0 = 4 * turn + sub;  // a lane's rows are 16 apart: the same place in the swizzle

@@ -233,3 +233,49 @@ def test_backward_with_gates_of_selections_that_nobody_lists(size):
             listed[drop] = False
             t, want[name], bound[name] = (v.reshape(-1)[listed] for v in (t, want[name], bound[name]))
         check(t, want[name], bound[name], name)
+
+
+@pytest.mark.parametrize("size", [(50, 64, 16, 8, 2), (400, 136, 200, 8, 2), (600, 320, 712, 3, 2)], ids=str)
+def test_a_slot_out_of_range_brings_in_no_token(size):
+    """A slot outside [0, N k) is skipped: an expert that lists one takes nothing of any token by it, whatever that token
+    holds."""
+    import mixture_experts_rank_b200 as more
+    N, h, s, M, k = size
+    args, d = make(*size)
+    X, d = args["X"].clone(), d.clone()
+    X[0], d[0] = NAN, NAN
+    slots, ends = args["slots"].clone(), args["offsets"].tolist()
+    mine = {e for e in range(M) if (slots[ends[e]:ends[e + 1]] // k == 0).any()}  # experts of token 0
+    others = [e for e in range(M) if e not in mine and ends[e + 1] - ends[e] > 2]
+    lost = []
+    for e, value in zip(others[:2], (N * k, -3)):
+        for at in (ends[e], ends[e + 1] - 1):  # the first, and the one that padding follows
+            lost.append(int(slots[at]))
+            slots[at] = value
+    assert lost
+    got = more.experts_backward(**dict(args, X=X, slots=slots), out_bar=d)
+    torch.cuda.synchronize()
+    assert more.device_status() != 0
+    gate = args["gate"].clone()
+    gate.view(-1)[lost] = 0
+    clean = dict(args, gate=gate)
+    clean["X"], dd = X.clone(), d.clone()
+    clean["X"][0], dd[0] = 0, 0
+    want, bound = ref.backward(**clean, out_bar=dd)
+    for i, name in ((1, "W_up_bar"), (2, "W_down_bar")):
+        check(got[i][others], want[name][others], bound[name][others], name)
+    check(got[0][1:], want["X_bar"][1:], bound["X_bar"][1:], "X_bar")
+
+
+@pytest.mark.parametrize("size", [(50, 64, 16, 8, 2), (400, 136, 200, 8, 2), (600, 320, 712, 3, 2)], ids=str)
+def test_an_infinite_gradient_stays_infinite(size):
+    """Rows are laid out in sixteens: what fills an expert's last one up has to add nothing, not zero times infinity."""
+    import mixture_experts_rank_b200 as more
+    N, h, s, M, k = size
+    args, d = make(*size)
+    d = d.clone()
+    e = int(torch.nonzero(args["offsets"].diff() % 16)[0])  # an expert whose rows do not fill their last sixteen
+    d[int(args["slots"][args["offsets"][e + 1] - 1]) // k, 3] = INF  # its last row
+    W_down_bar = more.experts_backward(**args, out_bar=d)[2]
+    assert ok()
+    assert (W_down_bar[e, 3].abs() == INF).all()
