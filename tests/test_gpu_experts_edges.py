@@ -1,4 +1,6 @@
 """The experts' operators where their numbers or sizes end."""
+import math
+
 import pytest
 import torch
 
@@ -279,3 +281,114 @@ def test_an_infinite_gradient_stays_infinite(size):
     W_down_bar = more.experts_backward(**args, out_bar=d)[2]
     assert ok()
     assert (W_down_bar[e, 3].abs() == INF).all()
+
+
+# ---- magnitudes and bits ------------------------------------------------------------------------------------------------
+ROWS = [(200, 136, 72, 8, 4), (300, 520, 64, 16, 8), (600, 320, 712, 3, 2), (1500, 264, 1032, 4, 2)]
+
+
+@pytest.mark.parametrize("size", ROWS, ids=str)
+@pytest.mark.parametrize("power", [-100, 100])
+def test_rows_of_any_magnitude(size, power):
+    """A power of two times the weights, or the gradient, is that power times the result."""
+    import mixture_experts_rank_b200 as more
+    args, d = make(*size)
+    want, wbar = more.experts(**args), more.experts_backward(**args, out_bar=d)[0]
+    out = more.experts(**dict(args, W_down=args["W_down"] * 2.0**power))
+    X_bar = more.experts_backward(**args, out_bar=d * 2.0**power)[0]
+    assert ok() and torch.equal(out, want * 2.0**power) and torch.equal(X_bar, wbar * 2.0**power)
+
+
+@pytest.mark.parametrize("size", ROWS, ids=str)
+@pytest.mark.parametrize("value", [2.0**-60, 2.0**60, 2.0**125, float("inf"), float("nan")])
+def test_columns_next_to_ones_of_another_magnitude(size, value):
+    """One output channel of a size of its own, or of no size at all, does not change its neighbours by more than the bf16
+    rounding of a row."""
+    import mixture_experts_rank_b200 as more
+    args, _ = make(*size)
+    h = size[1]
+    odd = [0, 70, h - 1]
+    W_down = args["W_down"].clone()
+    W_down[:, odd] = value
+    out = more.experts(**dict(args, W_down=W_down))
+    assert ok()
+    keep = torch.ones(h, dtype=torch.bool, device="cuda")
+    keep[odd] = False
+    want, bound = ref.forward(**args)
+    check(out[:, keep], want[:, keep], bound[:, keep], "out")
+    if abs(value) < 2.0**100:
+        want, bound = ref.forward(**dict(args, W_down=W_down))
+        check(out[:, odd], want[:, odd], bound[:, odd], "out of the odd channels")
+
+
+BITS = [(2000, 512, 64, 16, 4), (1000, 2048, 64, 16, 4), (500, 4096, 200, 8, 2), (1000, 1024, 40, 8, 8), (1000, 2048, 136, 8, 4),
+        (600, 320, 712, 3, 2)]
+
+
+@pytest.mark.parametrize("size", BITS, ids=str)
+def test_gate_gradients_of_long_products(size):
+    """The gates' gradient, an fp32 output, in the 2-norm.  The tensor cores cut a sum off at fp32's last place with every 16
+    products: on average half a place, 2^-24 of the sum so far, which is 2/3 of the whole sum's magnitude in the mean over
+    a sum of random signs.  Products of more than 2048, or of experts of up to 64 columns, are taken in runs of at most 1024.
+    Three such factors."""
+    import mixture_experts_rank_b200 as more
+    N, h, s, M, k = size
+    args, d = make(*size)
+    gate_bar = more.experts_backward(**args, out_bar=d)[3]
+    assert ok()
+    want = ref.backward(**args, out_bar=d)[0]["gate_bar"]
+    cuts = (min(h, 1024) if s <= 64 or h > 2048 else h) / 16
+    assert (gate_bar.double() - want).norm() <= 3 * cuts * 2.0**-24 * 2 / 3 * want.norm()
+
+
+@pytest.mark.parametrize("size", BITS, ids=str)
+def test_results_have_as_many_roundings_as_documented(size):
+    """In the 2-norm.  A rounding to bf16 is off by a uniform part of 2^-8 / m of a value with mantissa m; over mantissas of
+    even logarithm that is 2^-8 (1 / 3 * 3 / 8 / ln 2)^(1/2) = 0.00166 in the root mean square.  Three roundings: the middle
+    (or the gradients of a and b), a slot's row, the result; two for the weights' gradients, and in 8 bits; 5 percent for
+    the mantissas' distribution, where one rounding more would be 15 or 22."""
+    import mixture_experts_rank_b200 as more
+    args, d = make(*size)
+    once = 2.0**-8 * (1 / 3 * 3 / 8 / math.log(2)) ** 0.5
+
+    def holds(got, want, roundings):
+        return (got.double() - want).norm() <= 1.05 * once * roundings**0.5 * want.norm()
+
+    assert holds(more.experts(**args), ref.forward(**args)[0], 3)
+    got, want = more.experts_backward(**args, out_bar=d), ref.backward(**args, out_bar=d)[0]
+    assert holds(got[0], want["X_bar"], 3) and holds(got[1], want["W_up_bar"], 2) and holds(got[2], want["W_down_bar"], 2)
+    if size[1] % 16 == 0 and size[2] % 16 == 0:
+        args = int8_of(args)
+        assert holds(more.experts_int8(**args), ref.forward(**args)[0], 2)
+    assert ok()
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_wide_layers_on_two_streams_and_in_graphs(eight):
+    """Calls that take their channels in runs, with the shared memory of a whole SM and the whole GPU each: two at once, and
+    captured ones that share nothing but the device."""
+    import mixture_experts_rank_b200 as more
+    layer = more.moe_layer_int8 if eight else more.moe_layer
+    inputs = [layer_inputs(64, 7168, 16, 16, 32, seed) for seed in (0, 1)]
+    if eight:
+        inputs = [int8_of(a) for a in inputs]
+    want = [layer(**a, k=8) for a in inputs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in inputs]
+    got = [[], []]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(layer(**inputs[i], k=8))
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, want[i]) for i in (0, 1) for t in got[i])
+    graphs, held = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    for g, a in zip(graphs, inputs):
+        with torch.cuda.graph(g):
+            held.append(layer(**a, k=8))
+    for _ in range(2):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert ok() and all(torch.equal(t, w) for t, w in zip(held, want))
