@@ -19,7 +19,10 @@
 //   warps 4-11   epilogue, two warps a lane group.
 // The grid is persistent; tiles come from the row layout that the same call made on the device.
 // H and [da, db] are rounded to bf16: they are MMA operands.  Y and the rows of dx are rounded to bf16 before the
-// sum over a token's slots, which halves the traffic that bounds these kernels; the sum itself is in fp32.
+// sum over a token's slots, which halves the traffic that bounds these kernels; the sum itself is in fp32.  With the
+// result's own rounding that is 0.0029 in the 2-norm, one rounding fewer 0.0024.  To save one costs (prefill of 16384 tokens,
+// h = 2048, s = 64, M = 4096, and of 262144, h = 512: 900 and 922 us): H as a bf16 pair 963 and 1019 us; rows as fp16 with a
+// power of two for every 64 columns, 11 bits at the same traffic, 1045 and 1045 us, since the epilogue then binds.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -56,7 +59,9 @@ struct Shape {
   static constexpr bool kStaged = kIsDown || MODE == kDx || kIsDw;  // epilogue goes through shared memory
   // The tensor cores cut sums off, they do not round them: a sum over K comes out too small by about 1e-9 K of itself, and
   // the gate's gradient, which is fp32 to the end, by three times that.  Tiles of 3 x 64 columns therefore take their
-  // products in runs of kRun, added in registers; 3 x 128 columns are more than the registers hold.
+  // products in runs of kRun, added in registers; 3 x 128 columns are more than the registers hold.  Runs of 1024 leave
+  // 2.9e-6 in the 2-norm.  Runs of 256 would leave 7e-7, as sums in fp32 do, but their reads of the accumulators bind:
+  // backward at h = 512, s = 64 312 to 326 us, at h = 2048, s = 64 286 to 326 us, at h = 4096, s = 1024 963 to 1224 us.
   static constexpr bool kRuns = MODE == kBack && HALF == 64;
   // columns of one accumulator, and its place in TMEM
   static constexpr int kCols = kIsUp ? 2 * HALF : MODE == kBack ? 3 * HALF : 256;
@@ -1135,20 +1140,27 @@ struct Buffers {
 enum Kind { kForward = 0, kInt8 = 1, kBackward = 2 };
 
 // Tiles of the backward's first kernel: 3 x 128 columns, or 3 x 64 for experts that have no more, and where h is so long
-// that the products want runs (the gate's gradient is then off by 6e-6 of itself at most, as at h = 2048 in one run).
+// that the products want runs.  In one run the gate's gradient is off by 1.4e-6 of itself at h = 512 and 6.1e-6, the most, at
+// h = 2048; 3 x 64 columns from h = 512 on would halve that and take the backward of 8192 tokens, h = 2048, s = 1024,
+// from 1455 to 1780 us.
 int back_half(int h, int s) { return s <= 64 || h > 2 * kRun ? 64 : 128; }
 int gate_parts(int h, int s) { return 2 * tiles_of(s, back_half(h, s)); }
 
 // CTA pairs with 256-row tiles, the rows picked by token copied together first (the copies by token of a pair would
 // need both CTAs' loaders).  A pair reads the weights once for 256 rows, but the picked rows are written and read once
 // more, and tiles of 256 waste more of the last one.  us a call with and without pairs, for T rows an expert:
-//   forward   h = 2048: s = 256, T = 1024: 188, 153    s = 512, T = 1024: 136, 128    s = 1024, T = 2048: 428, 403
-//             s = 2048, T = 1024: 193, 202             h = 1096, s = 712, T = 469: 244, 265
-//             h = 4096, s = 4096, T = 1024: 336, 372
-//   8 bits    h = 2048: s = 512, T = 1024: 138, 126    s = 2048, T = 1500: 961, 1048    h = 2880 = s, T = 1024: 293, 339
+//   forward   h = 2048: s = 256, T = 1024: 188, 153    s = 512, T = 1024: 136, 128    s = 704, T = 512: 185, 172
+//             s = 1024, T = 256: 282, 263    T = 512: 462, 443    T = 1024: 408, 399    T = 2048: 380, 382
+//             s = 2048, T = 512: 421, 415    T = 1024: 370, 377   h = 1096, s = 712, T = 469: 217, 248
+//             h = 1024 = s, T = 512: 244, 238    h = 4096: s = 1024, T = 512: 448, 430    s = 4096, T = 1024: 336, 372
+//   8 bits    h = 2048: s = 512, T = 1024: 138, 126    s = 704, T = 512: 158, 153    s = 1024, T = 256: 206, 201
+//             T = 512: 331, 335    T = 2048: 295, 313    s = 2048, T = 1024: 286, 305    h = 2880 = s, T = 1024: 293, 339
+//             h = 1024 = s, T = 512: 231, 224    h = 4096, s = 1024, T = 2048: 265, 278
 //   backward  h = 1024: s = 144, T = 512: 437, 405     s = 512, T = 1024: 381, 409     s = 1024, T = 192: 216, 231
 //             s = 1024, T = 128: 206, 200              h = 2048, s = 1024, T = 2048: 1245, 1469
 //             h = 4096 (its first kernel takes no pairs): s = 512: 435, 428    s = 1024: 762, 785
+// The forward's border is a compromise: between s = 704 and 2048 pairs lose up to 7 % where sizes fill tiles of 128, and win
+// 12 % where they do not.
 bool takes_pairs(int64_t S, int h, int s, int M, int kind) {
   return S >= 192 * (int64_t)M && s >= (kind == kBackward && h <= 2 * kRun ? 512 : 704);
 }
